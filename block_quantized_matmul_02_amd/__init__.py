@@ -2,7 +2,8 @@
 
 Argument marshalling only: every step runs in the HIP kernels of
 ``libbqmm.so`` (built in-tree by ``block_quantized_matmul_02_amd.build``).
-The functions carry the C ABI's names (``include/bqmm.h``), take torch
+The functions carry the C ABI's names (``include/bqmm.h`` and, for the
+operators around the matmul, ``include/bqmm_layer.h``), take torch
 tensors that live on the GPU, enqueue on torch's current stream and never
 synchronize.  There is no CPU fallback: a missing library raises.
 """
@@ -20,6 +21,11 @@ BQM_EUNSUPPORTED = 2
 BQM_EHIP_BASE = 10000
 GEMV_MAX_M = 15
 E4M3_GEMV_MAX_M = 16
+MXFP4_GEMV_MAX_M = 16
+LOGPROBS_MAX_TOP = 32
+BQM_F32 = 0
+BQM_F16 = 1
+BQM_BF16 = 2
 
 _lib = None
 
@@ -58,6 +64,19 @@ def lib() -> ctypes.CDLL:
                    "bqm_e4m3_gemm", "bqm_e4m3_gemv", "bqm_q8_0_dequant_f16", "bqm_f16_cvt", "bqm_f16_gemm",
                    "bqm_q8_0_gemm_f8acc", "bqm_e4m3_nan_count", "bqm_e4m3_blk_quantize", "bqm_e4m3_blk_gemm",
                    "bqm_q8_0_gemv_f32", "bqm_e4m3_gemm_exact"):
+            getattr(L, fn).restype = ctypes.c_int
+        L.bqm_add_rmsnorm.argtypes = [P, I64, P, I64, P, F, P, I64, P, I, I, I, I, P]
+        L.bqm_add_rmsnorm_q8_1.argtypes = [P, I64, P, I64, P, F, P, I64, P, P, I, I, I, P]
+        L.bqm_add_rmsnorm_e4m3_blk.argtypes = [P, I64, P, I64, P, F, P, I64, P, P, I, I, I, P]
+        L.bqm_mxfp4_quantize.argtypes = [P, I64, P, P, I, I, I, P]
+        L.bqm_mxfp4_dequantize.argtypes = [P, P, P, I, I, I, P]
+        L.bqm_mxfp4_gemm.argtypes = [P, P, P, P, P, I, I, I, P]
+        L.bqm_mxfp4_gemv.argtypes = [P, P, P, P, I, I, I, P]
+        L.bqm_logprobs.argtypes = [P, I64, I, P, I, P, P, P, P, P, I, P, I, I, P]
+        L.bqm_logprobs_workspace.argtypes = [I, I, I]
+        L.bqm_logprobs_workspace.restype = I64
+        for fn in ("bqm_add_rmsnorm", "bqm_add_rmsnorm_q8_1", "bqm_add_rmsnorm_e4m3_blk", "bqm_mxfp4_quantize",
+                   "bqm_mxfp4_dequantize", "bqm_mxfp4_gemm", "bqm_mxfp4_gemv", "bqm_logprobs"):
             getattr(L, fn).restype = ctypes.c_int
         L.bqm_strerror.argtypes = [I]
         L.bqm_strerror.restype = ctypes.c_char_p
@@ -328,3 +347,222 @@ def bqm_e4m3_blk_gemm(w, grid, xq, xs, y=None):
     _raise("bqm_e4m3_blk_gemm", lib().bqm_e4m3_blk_gemm(_ptr(w), _ptr(grid), _ptr(xq), _ptr(xs), _ptr(y), m, k, n,
                                                         _stream(w)))
     return y
+
+
+# ------------------------------------------- the operators around the matmul
+
+
+def _type(t, name):
+    import torch
+
+    code = {torch.float32: BQM_F32, torch.float16: BQM_F16, torch.bfloat16: BQM_BF16}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    return code
+
+
+def _rows(t, name, dtype=None, shape=None):
+    """Checks a 2-D GPU tensor whose rows are contiguous; returns its row stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must have shape {shape or '[rows, columns]'}, got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.stride(0)
+
+
+def _optr(t):
+    return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _norm_args(x, res, gain, h):
+    """The arguments that the three norms share: x .. gain, and h with its stride."""
+    import torch
+
+    ldx = _rows(x, "x")
+    _type(x, "x")
+    if gain is not None:
+        _check(gain, torch.float32, "gain", (x.shape[1],))
+    if res is None:
+        if h is not None:
+            raise ValueError("h is the sum x + res: it goes with res")
+        return (_ptr(x), ldx, None, 0, _optr(gain)), (None, 0), None
+    ldr = _rows(res, "res", x.dtype, x.shape)
+    if h is None:
+        h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    ldh = _rows(h, "h", x.dtype, x.shape)
+    return (_ptr(x), ldx, _ptr(res), ldr, _optr(gain)), (_ptr(h), ldh), h
+
+
+def bqm_add_rmsnorm(x, res=None, gain=None, eps: float = 1e-6, h=None, y=None, out_dtype=None):
+    """RMS norm of ``x [m, k]`` or of ``x + res`` -> (``y [m, k]``, ``h = x + res`` or None).
+
+    x, res and h are f32, fp16 or bf16 alike, with any row stride; ``gain`` is f32 ``[k]`` or None for ones.
+    y is f32 or x's type (``out_dtype``, f32 if not given); h may be x or res itself.
+    """
+    import torch
+
+    m, k = x.shape
+    head, tail, h = _norm_args(x, res, gain, h)
+    if y is None:
+        y = torch.empty((m, k), dtype=out_dtype or torch.float32, device=x.device)
+    _check(y, out_dtype or y.dtype, "y", (m, k))
+    _raise("bqm_add_rmsnorm", lib().bqm_add_rmsnorm(*head, eps, *tail, _ptr(y), _type(x, "x"), _type(y, "y"), m, k,
+                                                    _stream(x)))
+    return y, h
+
+
+def bqm_add_rmsnorm_q8_1(x, res=None, gain=None, eps: float = 1e-6, h=None, xq=None, xds=None):
+    """RMS norm as :func:`bqm_add_rmsnorm`, written as the q8_1 operand of bqm_q8_0_gemv / bqm_q8_0_gemm:
+    (int8 ``xq [m, k]``, f32 ``xds [m, k/32, 2]``, ``h`` or None)."""
+    import torch
+
+    m, k = x.shape
+    head, tail, h = _norm_args(x, res, gain, h)
+    if xq is None:
+        xq = torch.empty((m, k), dtype=torch.int8, device=x.device)
+    if xds is None:
+        xds = torch.empty((m, k // 32, 2), dtype=torch.float32, device=x.device)
+    _check(xq, torch.int8, "xq", (m, k))
+    _check(xds, torch.float32, "xds", (m, k // 32, 2))
+    _raise("bqm_add_rmsnorm_q8_1", lib().bqm_add_rmsnorm_q8_1(*head, eps, *tail, _ptr(xq), _ptr(xds), _type(x, "x"),
+                                                              m, k, _stream(x)))
+    return xq, xds, h
+
+
+def bqm_add_rmsnorm_e4m3_blk(x, res=None, gain=None, eps: float = 1e-6, h=None, xq=None, xs=None):
+    """RMS norm as :func:`bqm_add_rmsnorm`, written as the operand of bqm_e4m3_blk_gemm:
+    (e4m3 codes ``xq [m, k]``, f32 ``xs [m, ceil(k/128)]``, ``h`` or None)."""
+    import torch
+
+    m, k = x.shape
+    head, tail, h = _norm_args(x, res, gain, h)
+    if xq is None:
+        xq = torch.empty((m, k), dtype=torch.uint8, device=x.device)
+    if xs is None:
+        xs = torch.empty((m, (k + 127) // 128), dtype=torch.float32, device=x.device)
+    _check(xq, torch.uint8, "xq", (m, k))
+    _check(xs, torch.float32, "xs", (m, (k + 127) // 128))
+    _raise("bqm_add_rmsnorm_e4m3_blk",
+           lib().bqm_add_rmsnorm_e4m3_blk(*head, eps, *tail, _ptr(xq), _ptr(xs), _type(x, "x"), m, k, _stream(x)))
+    return xq, xs, h
+
+
+def bqm_mxfp4_quantize(x, codes=None, scales=None):
+    """MXFP4 quantization of ``x [m, k]`` (f32, fp16 or bf16, any row stride) -> (uint8 ``codes [m, k/2]``,
+    E8M0 ``scales [m, k/32]``)."""
+    import torch
+
+    m, k = x.shape
+    ldx = _rows(x, "x")
+    if codes is None:
+        codes = torch.empty((m, k // 2), dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = torch.empty((m, k // 32), dtype=torch.uint8, device=x.device)
+    _check(codes, torch.uint8, "codes", (m, k // 2))
+    _check(scales, torch.uint8, "scales", (m, k // 32))
+    _raise("bqm_mxfp4_quantize", lib().bqm_mxfp4_quantize(_ptr(x), ldx, _ptr(codes), _ptr(scales), _type(x, "x"), m, k,
+                                                          _stream(x)))
+    return codes, scales
+
+
+def bqm_mxfp4_dequantize(codes, scales, dtype=None, y=None):
+    """The values of MXFP4 ``codes [m, k/2]`` and ``scales [m, k/32]`` -> ``y [m, k]`` (f32 if no ``dtype``)."""
+    import torch
+
+    _check(codes, torch.uint8, "codes")
+    m, k = codes.shape[0], codes.shape[1] * 2
+    _check(scales, torch.uint8, "scales", (m, k // 32))
+    if y is None:
+        y = torch.empty((m, k), dtype=dtype or torch.float32, device=codes.device)
+    _check(y, dtype or y.dtype, "y", (m, k))
+    _raise("bqm_mxfp4_dequantize", lib().bqm_mxfp4_dequantize(_ptr(codes), _ptr(scales), _ptr(y), _type(y, "y"), m, k,
+                                                              _stream(codes)))
+    return y
+
+
+def bqm_mxfp4_gemm(w, ws, xq, xs, y=None):
+    """MXFP4 x MXFP4 GEMM, any m: weights ``w [n, k/2]``, ``ws [n, k/32]`` and activations ``xq [m, k/2]``,
+    ``xs [m, k/32]`` -> f32 ``y [m, n]``."""
+    import torch
+
+    n, half = w.shape
+    m, k = xq.shape[0], 2 * half
+    _check(w, torch.uint8, "w")
+    _check(ws, torch.uint8, "ws", (n, k // 32))
+    _check(xq, torch.uint8, "xq", (m, half))
+    _check(xs, torch.uint8, "xs", (m, k // 32))
+    if y is None:
+        y = torch.empty((m, n), dtype=torch.float32, device=xq.device)
+    _check(y, torch.float32, "y", (m, n))
+    _raise("bqm_mxfp4_gemm", lib().bqm_mxfp4_gemm(_ptr(w), _ptr(ws), _ptr(xq), _ptr(xs), _ptr(y), m, k, n, _stream(w)))
+    return y
+
+
+def bqm_mxfp4_gemv(w, ws, x, y=None):
+    """MXFP4 decode GEMV, 1 <= m <= 16: weights ``w [n, k/2]``, ``ws [n, k/32]`` against f32 ``x [m, k]``
+    -> f32 ``y [m, n]``."""
+    import torch
+
+    n, half = w.shape
+    m, k = x.shape[0], 2 * half
+    _check(w, torch.uint8, "w")
+    _check(ws, torch.uint8, "ws", (n, k // 32))
+    _check(x, torch.float32, "x", (m, k))
+    if y is None:
+        y = torch.empty((m, n), dtype=torch.float32, device=x.device)
+    _check(y, torch.float32, "y", (m, n))
+    _raise("bqm_mxfp4_gemv", lib().bqm_mxfp4_gemv(_ptr(w), _ptr(ws), _ptr(x), _ptr(y), m, k, n, _stream(w)))
+    return y
+
+
+def bqm_logprobs_workspace(m: int, n: int, top_k: int) -> int:
+    """Bytes of workspace that :func:`bqm_logprobs` needs for ``m`` rows of ``n`` logits."""
+    size = lib().bqm_logprobs_workspace(m, n, top_k)
+    if size < 0:
+        raise BqmError("bqm_logprobs_workspace", BQM_EINVAL)
+    return size
+
+
+def bqm_logprobs(logits, tokens=None, top_k: int = 0, out=None, workspace=None):
+    """Log probabilities of int32 ``tokens [m, t]`` under ``logits [m, n]`` (f32, fp16 or bf16, any row stride),
+    with each row's log-sum-exp, entropy and ``top_k`` alternatives.
+
+    -> (``logp [m, t]``, ``lse [m]``, ``entropy [m]``, int32 ``top_ids [m, top_k]``, ``top_logp [m, top_k]``);
+    ``out`` is such a tuple to write into, ``workspace`` uint8 of at least :func:`bqm_logprobs_workspace` bytes.
+    """
+    import torch
+
+    m, n = logits.shape
+    ld = _rows(logits, "logits")
+    t = 0
+    if tokens is not None:
+        if tokens.dim() != 2:
+            raise ValueError(f"tokens must be [m, t], got {tuple(tokens.shape)}")
+        t = tokens.shape[1]
+        _check(tokens, torch.int32, "tokens", (m, t))
+    if out is None:
+        f = dict(dtype=torch.float32, device=logits.device)
+        out = (torch.empty((m, t), **f), torch.empty(m, **f), torch.empty(m, **f),
+               torch.empty((m, max(top_k, 0)), dtype=torch.int32, device=logits.device),
+               torch.empty((m, max(top_k, 0)), **f))
+    logp, lse, entropy, ids, top = out
+    _check(logp, torch.float32, "logp", (m, t))
+    _check(lse, torch.float32, "lse", (m,))
+    _check(entropy, torch.float32, "entropy", (m,))
+    _check(ids, torch.int32, "top_ids", (m, max(top_k, 0)))
+    _check(top, torch.float32, "top_logp", (m, max(top_k, 0)))
+    need = bqm_logprobs_workspace(m, n, top_k)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
+    if workspace is not None:
+        _check(workspace, torch.uint8, "workspace")
+        if workspace.numel() < need:
+            raise ValueError(f"workspace must hold {need} bytes, got {workspace.numel()}")
+    _raise("bqm_logprobs", lib().bqm_logprobs(_ptr(logits), ld, _type(logits, "logits"), _optr(tokens), t, _ptr(logp),
+                                              _ptr(lse), _ptr(entropy), _ptr(ids), _ptr(top), top_k,
+                                              _optr(workspace), m, n, _stream(logits)))
+    return logp, lse, entropy, ids, top

@@ -1,0 +1,39 @@
+// Typed loads and stores of the kernels that take f32, fp16 or bf16 values.
+#pragma once
+
+#include "bqmm_internal.h"
+#include "bqmm_layer.h"
+
+namespace bqm {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v8f __attribute__((ext_vector_type(8)));
+
+template <typename T> struct Vec;
+template <> struct Vec<float> {
+    typedef float x4 __attribute__((ext_vector_type(4)));
+    typedef float x8 __attribute__((ext_vector_type(8)));
+};
+template <> struct Vec<_Float16> {
+    typedef _Float16 x4 __attribute__((ext_vector_type(4)));
+    typedef _Float16 x8 __attribute__((ext_vector_type(8)));
+};
+template <> struct Vec<__bf16> {
+    typedef __bf16 x4 __attribute__((ext_vector_type(4)));
+    typedef __bf16 x8 __attribute__((ext_vector_type(8)));
+};
+
+inline int type_bytes(int type) { return type == BQM_F32 ? 4 : 2; }
+inline bool type_known(int type) { return type == BQM_F32 || type == BQM_F16 || type == BQM_BF16; }
+
+// Largest magnitude over a row of 16 lanes, on every lane (magnitudes only:
+// a NaN operand is dropped).
+__device__ __forceinline__ float dpp_absmax16(float v) {
+    v = q8_1_max8(v);
+    return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x140, 0xF, 0xF, false)));
+}
+
+// Sum over the wave, on every lane.
+__device__ __forceinline__ float wave_sum(float v) { return swap32_sum(swap16_sum(dpp_sum16(v))); }
+
+}  // namespace bqm
