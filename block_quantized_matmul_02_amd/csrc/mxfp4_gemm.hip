@@ -14,13 +14,18 @@ namespace bqm {
 
 constexpr int kMgStage = 256;                 // k of an LDS stage: 8 scale blocks, 4 MFMA steps
 constexpr int kMgRowBytes = kMgStage / 2;
-constexpr int kMgRowStride = kMgRowBytes + 16;   // padded LDS row: conflict-free 16-byte reads
+constexpr int kMgSuper = 4;                   // stages whose scales are staged together: 32 bytes a row
 
 struct MgArgs {
     const uint8_t *w, *ws, *xq, *xs;
     float *y;
+    int64_t ldy;          // floats between rows of y
     int m, k, n;
+    int mtiles, ntiles;
 };
+
+constexpr int kMgLargeM = 192, kMgLargeN = 256;   // the large tile: 8 waves of 96 x 64
+constexpr int kMgSmall = 128;                     // the small one: 4 waves of 64 x 64
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t mg_rsrc(const void *base, int64_t bytes) {
     const uint32_t b = bytes <= 0 ? 0u : bytes > 0x7FFFFFF0ll ? 0x7FFFFFF0u : (uint32_t)bytes;
@@ -35,22 +40,39 @@ __device__ __forceinline__ v16f mg_mfma(u32x4 a, u32x4 b, v16f c, int sa, int sb
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(va, vb, c, 4, 4, Q, sa, Q, sb);
 }
 
+// Tile of workgroup id.  Workgroups reach the eight XCDs round-robin; of each
+// 256 consecutive ones (a round, one per compute unit) an XCD's 32 take tiles
+// that follow each other down strips of eight tile rows, so that its L2 serves
+// each operand row to several of them.
+__device__ __forceinline__ void mg_tile(int id, int mtiles, int ntiles, int &mt, int &nt) {
+    const int base = id & ~255, r = id & 255;
+    if (base + 256 <= mtiles * ntiles) id = base + (r & 7) * 32 + (r >> 3);
+    const int strip = id / (8 * ntiles), in = id - strip * 8 * ntiles;
+    const int high = min(8, mtiles - 8 * strip);
+    mt = 8 * strip + in % high;
+    nt = in / high;
+}
+
 // WM x WN waves, each TM x TN tiles of 32 x 32 (tokens x weight rows).
-// WIDE: scale rows are whole, aligned dwords (k % 128 == 0); else bytes.
-template <int WM, int WN, int TM, int TN, bool WIDE>
+// SW: bytes of the loads that scale rows are aligned to (16, 4 or 1).
+template <int WM, int WN, int TM, int TN, int SW>
 __global__ __launch_bounds__(64 * WM * WN) void mxfp4_gemm_kernel(MgArgs a) {
-    constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN, NT = 64 * WM * WN;
+    constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN, NT = 64 * WM * WN, ROWS = BM + BN;
     constexpr int CA = BM * 8 / NT, CB = BN * 8 / NT;   // 16-byte chunks per thread and stage
     constexpr int RS = NT / 8;                          // rows between a thread's chunks
-    __shared__ __attribute__((aligned(16))) uint8_t st[2][(BM + BN) * kMgRowStride];
+    constexpr int SR = (ROWS + NT - 1) / NT;            // scale rows per thread
+    __shared__ __attribute__((aligned(16))) uint8_t st[2][ROWS * kMgRowBytes];
+    __shared__ int sc[2][2 * kMgSuper][SR * NT];   // scale dword j (blocks 4j .. 4j+3 of the superstage) of each row
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const int r32 = lane & 31, g = lane >> 5;
-    const int64_t m0 = (int64_t)blockIdx.y * BM, n0 = (int64_t)blockIdx.x * BN;
+    int mt, nt;
+    mg_tile(blockIdx.x, a.mtiles, a.ntiles, mt, nt);
+    const int64_t m0 = (int64_t)mt * BM, n0 = (int64_t)nt * BN;
     const int64_t rb = a.k / 2;
     const int nblk = a.k / 32;
-    const int stages = (nblk + 7) / 8;
+    const int supers = (nblk + 8 * kMgSuper - 1) / (8 * kMgSuper);
 
     const int64_t rowsA = a.m - m0 < BM ? a.m - m0 : BM, rowsB = a.n - n0 < BN ? a.n - n0 : BN;
     const __amdgpu_buffer_rsrc_t rA = mg_rsrc(a.xq + m0 * rb, rowsA * rb);
@@ -58,47 +80,72 @@ __global__ __launch_bounds__(64 * WM * WN) void mxfp4_gemm_kernel(MgArgs a) {
     const __amdgpu_buffer_rsrc_t rSA = mg_rsrc(a.xs + m0 * nblk, rowsA * nblk);
     const __amdgpu_buffer_rsrc_t rSB = mg_rsrc(a.ws + n0 * nblk, rowsB * nblk);
 
-    // thread: row tid / 8 (+ RS per chunk), 16-byte chunk tid % 8 of the stage
+    struct Regs {
+        u32x4 a[CA], b[CB];
+    };
+    // thread: row tid / 8 (+ RS per chunk), 16-byte chunk tid % 8 of the stage,
+    // stored at slot chunk ^ (row % 8) so that eight rows' reads of one chunk
+    // meet eight different slots
     const int chunk = tid & 7, row = tid >> 3;
-    u32x4 ca[CA], cb[CB];
-    auto load = [&](int s) {
-        // chunks past the row's end are read as zeros
+    // stages past the last read zeros
+    auto load = [&](Regs &R, int s) {
         const uint32_t off = 8 * s + chunk < nblk ? (uint32_t)(row * rb + 16 * (8 * s + chunk)) : 0x80000000u;
 #pragma unroll
         for (int i = 0; i < CA; i++)
-            ca[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rA, off + (uint32_t)(i * RS * rb), 0, 0));
+            R.a[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rA, off + (uint32_t)(i * RS * rb), 0, 0));
 #pragma unroll
         for (int i = 0; i < CB; i++)
-            cb[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rB, off + (uint32_t)(i * RS * rb), 0, 0));
+            R.b[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rB, off + (uint32_t)(i * RS * rb), 0, 0));
     };
-    auto store = [&](uint8_t *p) {
-        const int at = row * kMgRowStride + 16 * chunk;
+    auto store = [&](uint8_t *p, const Regs &R) {
+        const int at = row * kMgRowBytes + 16 * (chunk ^ (row & 7));
 #pragma unroll
-        for (int i = 0; i < CA; i++) *reinterpret_cast<u32x4 *>(p + at + i * RS * kMgRowStride) = ca[i];
+        for (int i = 0; i < CA; i++) *reinterpret_cast<u32x4 *>(p + at + i * RS * kMgRowBytes) = R.a[i];
 #pragma unroll
-        for (int i = 0; i < CB; i++) *reinterpret_cast<u32x4 *>(p + at + (BM + i * RS) * kMgRowStride) = cb[i];
+        for (int i = 0; i < CB; i++) *reinterpret_cast<u32x4 *>(p + at + (BM + i * RS) * kMgRowBytes) = R.b[i];
     };
-    // lane half g takes scale blocks 4g .. 4g+3 of a stage, one per step, so
-    // its four scales of a row are one dword
-    auto scales = [&](const __amdgpu_buffer_rsrc_t &r, int row0, int s) {
-        const int b = 8 * s + 4 * g;
-        const uint32_t at = (uint32_t)((row0 + r32) * nblk + b);
-        if constexpr (WIDE) {
-            return (int)__builtin_amdgcn_raw_buffer_load_b32(r, b < nblk ? at : 0x80000000u, 0, 0);
-        } else {
-            unsigned v = 0;
+    // Scales: a thread loads the 32 bytes of a row that four stages need.
+    struct ScaleRegs {
+        unsigned v[SR][2 * kMgSuper];
+    };
+    auto load_scales = [&](ScaleRegs &S, int super) {
+        const int b0 = 8 * kMgSuper * super;
 #pragma unroll
-            for (int q = 0; q < 4; q++)
-                v |= (unsigned)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, b + q < nblk ? at + q : 0x80000000u, 0, 0) << (8 * q);
-            return (int)v;
+        for (int i = 0; i < SR; i++) {
+            const int rr = tid + i * NT;
+            const bool isA = rr < BM;   // uniform: BM is a multiple of the wave
+            const __amdgpu_buffer_rsrc_t r = isA ? rSA : rSB;
+            const uint32_t at = (uint32_t)((isA ? rr : rr - BM) * nblk + b0);
+            if constexpr (SW == 16) {
+#pragma unroll
+                for (int q = 0; q < 2; q++) {
+                    const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                        r, b0 + 16 * q < nblk ? at + 16 * q : 0x80000000u, 0, 0));
+#pragma unroll
+                    for (int e = 0; e < 4; e++) S.v[i][4 * q + e] = v[e];
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < 2 * kMgSuper; q++) {
+                    const int b = 4 * q;
+                    if constexpr (SW == 4) {
+                        S.v[i][q] = __builtin_amdgcn_raw_buffer_load_b32(r, b0 + b < nblk ? at + b : 0x80000000u, 0, 0);
+                    } else {
+                        S.v[i][q] = 0;
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            S.v[i][q] |= (unsigned)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
+                                             r, b0 + b + e < nblk ? at + b + e : 0x80000000u, 0, 0) << (8 * e);
+                    }
+                }
+            }
         }
     };
-    int sa[TM], sb[TN];
-    auto load_scales = [&](int s) {
+    auto store_scales = [&](const ScaleRegs &S, int buf) {
 #pragma unroll
-        for (int i = 0; i < TM; i++) sa[i] = scales(rSA, wm * 32 * TM + 32 * i, s);
+        for (int i = 0; i < SR; i++)
 #pragma unroll
-        for (int j = 0; j < TN; j++) sb[j] = scales(rSB, wn * 32 * TN + 32 * j, s);
+            for (int q = 0; q < 2 * kMgSuper; q++) sc[buf][q][tid + i * NT] = (int)S.v[i][q];
     };
 
     v16f acc[TM][TN];
@@ -109,42 +156,100 @@ __global__ __launch_bounds__(64 * WM * WN) void mxfp4_gemm_kernel(MgArgs a) {
 #pragma unroll
             for (int v = 0; v < 16; v++) acc[i][j][v] = 0.0f;
 
-    load(0);
-    load_scales(0);
-    store(st[0]);
+    // Operands of a step and scales of a stage, read one step ahead.  Lane half
+    // g takes chunks 4g .. 4g+3 of a stage, one per step, so its four scales
+    // of a row are one dword.
+    const int rowA = wm * 32 * TM + r32, rowB = BM + wn * 32 * TN + r32;
+    u32x4 va[2][TM], vb[2][TN];
+    int ta[2][TM], tb[2][TN];
+    auto read = [&](const uint8_t *p, auto q) {
+        constexpr int Q = decltype(q)::value;
+        const int slot = 16 * ((4 * g + Q) ^ (r32 & 7));
+#pragma unroll
+        for (int i = 0; i < TM; i++) va[Q & 1][i] = *reinterpret_cast<const u32x4 *>(p + (rowA + 32 * i) * kMgRowBytes + slot);
+#pragma unroll
+        for (int j = 0; j < TN; j++) vb[Q & 1][j] = *reinterpret_cast<const u32x4 *>(p + (rowB + 32 * j) * kMgRowBytes + slot);
+    };
+    auto read_scales = [&](const int (*scales)[SR * NT], int slot) {
+#pragma unroll
+        for (int i = 0; i < TM; i++) ta[slot][i] = scales[g][rowA + 32 * i];
+#pragma unroll
+        for (int j = 0; j < TN; j++) tb[slot][j] = scales[g][rowB + 32 * j];
+    };
+    auto multiply = [&](auto q, int slot) {
+        constexpr int Q = decltype(q)::value;
+#pragma unroll
+        for (int i = 0; i < TM; i++)
+#pragma unroll
+            for (int j = 0; j < TN; j++) acc[i][j] = mg_mfma<Q>(va[Q & 1][i], vb[Q & 1][j], acc[i][j], ta[slot][i], tb[slot][j]);
+    };
+    constexpr std::integral_constant<int, 0> q0{};
+    constexpr std::integral_constant<int, 1> q1{};
+    constexpr std::integral_constant<int, 2> q2{};
+    constexpr std::integral_constant<int, 3> q3{};
+
+    Regs R;
+    ScaleRegs S;
+    load_scales(S, 0);
+    load(R, 0);
+    store_scales(S, 0);
+    store(st[0], R);
+    load(R, 1);
     __syncthreads();
-    for (int s = 0; s < stages; s++) {
-        const uint8_t *const pa = st[s & 1] + (wm * 32 * TM + r32) * kMgRowStride + 64 * g;
-        const uint8_t *const pb = st[s & 1] + (BM + wn * 32 * TN + r32) * kMgRowStride + 64 * g;
-        int ta[TM], tb[TN];
+    read(st[0], q0);
+    read_scales(&sc[0][0], 0);
+    // Stage s = 4 super + J is in st[J & 1], its first operands are in
+    // registers, and stage s + 1 is on its way to R.  The
+    // barrier stands before the last step: by then every wave has read this
+    // stage's operands and stored its share of the next one, whose first
+    // operands arrive while the last step multiplies.  The next superstage's
+    // scales are loaded in a superstage's first stage and stored in its third.
+    auto stage = [&](int s, auto pos, int super) {
+        constexpr int J = decltype(pos)::value;
+        uint8_t *const here = st[J & 1], *const there = st[(J + 1) & 1];
+        if constexpr (J == 0) load_scales(S, super + 1);
+        read(here, q1);
+        multiply(q0, J & 1);
+        read(here, q2);
+        multiply(q1, J & 1);
+        store(there, R);
+        if constexpr (J == 2) store_scales(S, (super + 1) & 1);
+        load(R, s + 2);
+        read(here, q3);
+        multiply(q2, J & 1);
+        // LDS accesses between the MFMAs: an even share of the three steps'
+        // reads after each, and of the writes after those of the last two
 #pragma unroll
-        for (int i = 0; i < TM; i++) ta[i] = sa[i];
-#pragma unroll
-        for (int j = 0; j < TN; j++) tb[j] = sb[j];
-        if (s + 1 < stages) {
-            load(s + 1);
-            load_scales(s + 1);
+        for (int r = 0; r < 3 * TM * TN; r++) {
+            if (r == 0) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, (TM + TN + TM * TN - 1) / (TM * TN), 0);
+            if (r >= TM * TN) __builtin_amdgcn_sched_group_barrier(0x200, (CA + CB + 2 * TM * TN - 1) / (2 * TM * TN), 0);
         }
-        auto step = [&](auto q) {
-            constexpr int Q = decltype(q)::value;
-            u32x4 va[TM], vb[TN];
-#pragma unroll
-            for (int i = 0; i < TM; i++) va[i] = *reinterpret_cast<const u32x4 *>(pa + i * 32 * kMgRowStride + 16 * Q);
-#pragma unroll
-            for (int j = 0; j < TN; j++) vb[j] = *reinterpret_cast<const u32x4 *>(pb + j * 32 * kMgRowStride + 16 * Q);
-#pragma unroll
-            for (int i = 0; i < TM; i++)
-#pragma unroll
-                for (int j = 0; j < TN; j++) acc[i][j] = mg_mfma<Q>(va[i], vb[j], acc[i][j], ta[i], tb[j]);
-        };
-        step(std::integral_constant<int, 0>{});
-        step(std::integral_constant<int, 1>{});
-        step(std::integral_constant<int, 2>{});
-        step(std::integral_constant<int, 3>{});
-        if (s + 1 < stages) store(st[(s + 1) & 1]);
         __syncthreads();
+        read(there, q0);
+        read_scales(J == 3 ? &sc[(super + 1) & 1][0] : &sc[super & 1][2 * ((J + 1) & 3)], (J + 1) & 1);
+        multiply(q3, J & 1);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+#pragma unroll
+        for (int r = 0; r < TM * TN; r++) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2 * (TM + TN) / (TM * TN) + 1, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);   // nothing of the next stage moves up
+    };
+    // whole superstages: the stages past the row's end multiply zeros
+#pragma unroll 1
+    for (int super = 0; super < supers; super++) {
+        const int s = super * kMgSuper;
+        stage(s, q0, super);
+        stage(s + 1, q1, super);
+        stage(s + 2, q2, super);
+        stage(s + 3, q3, super);
     }
 
+    // Lane: column r32, rows 8 (v / 4) + 4 g + v % 4.  y is written past the
+    // caches: nothing here reads it again, and the operands keep their room.
 #pragma unroll
     for (int i = 0; i < TM; i++)
 #pragma unroll
@@ -154,22 +259,55 @@ __global__ __launch_bounds__(64 * WM * WN) void mxfp4_gemm_kernel(MgArgs a) {
 #pragma unroll
             for (int v = 0; v < 16; v++) {
                 const int64_t t = m0 + wm * 32 * TM + i * 32 + 8 * (v >> 2) + 4 * g + (v & 3);
-                if (t < a.m) a.y[t * a.n + col] = acc[i][j][v];
+                if (t < a.m) __builtin_nontemporal_store(acc[i][j][v], a.y + t * a.ldy + col);
             }
         }
 }
 
 template <int WM, int WN, int TM, int TN>
-static int launch_mg(const MgArgs &a, hipStream_t s) {
-    constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN;
-    const dim3 grid((a.n + BN - 1) / BN, (a.m + BM - 1) / BM);
-    // the dispatch counts rows of tiles in 16 bits and work items in 32
-    if (grid.y > 65535 || (int64_t)grid.x * (64 * WM * WN) > 0xFFFFFFFFll) return BQM_EUNSUPPORTED;
-    if (a.k % 128 == 0 && aligned(a.ws, 4) && aligned(a.xs, 4))
-        hipLaunchKernelGGL((mxfp4_gemm_kernel<WM, WN, TM, TN, true>), grid, dim3(64 * WM * WN), 0, s, a);
+static int launch_mg(MgArgs a, hipStream_t s) {
+    constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN, NT = 64 * WM * WN;
+    a.mtiles = (a.m + BM - 1) / BM;
+    a.ntiles = (a.n + BN - 1) / BN;
+    const int64_t grid = (int64_t)a.mtiles * a.ntiles;
+    if (grid * NT > 0xFFFFFFFFll) return BQM_EUNSUPPORTED;   // the dispatch counts work items in 32 bits
+    const int nblk = a.k / 32;
+    if (nblk % 16 == 0 && aligned(a.ws, 16) && aligned(a.xs, 16))
+        hipLaunchKernelGGL((mxfp4_gemm_kernel<WM, WN, TM, TN, 16>), dim3((unsigned)grid), dim3(NT), 0, s, a);
+    else if (nblk % 4 == 0 && aligned(a.ws, 4) && aligned(a.xs, 4))
+        hipLaunchKernelGGL((mxfp4_gemm_kernel<WM, WN, TM, TN, 4>), dim3((unsigned)grid), dim3(NT), 0, s, a);
     else
-        hipLaunchKernelGGL((mxfp4_gemm_kernel<WM, WN, TM, TN, false>), grid, dim3(64 * WM * WN), 0, s, a);
+        hipLaunchKernelGGL((mxfp4_gemm_kernel<WM, WN, TM, TN, 1>), dim3((unsigned)grid), dim3(NT), 0, s, a);
     return launch_status();
+}
+
+// Estimated microseconds (measured at k = 4096, 5120 and 8192): the large tile
+// takes 1.2 per stage and 11 besides for each round of one per compute unit;
+// the small one, two to a compute unit, 0.65 and 1.2 for each that a compute
+// unit gets, or 0.8 and 2 if it gets a single one.
+static double large_cost(int64_t rounds, int stages) { return rounds * (1.2 * stages + 11.0); }
+static double small_cost(int64_t each, int stages) {
+    return each == 0 ? 0.0 : each == 1 ? 0.8 * stages + 2.0 : each * (0.65 * stages + 1.2);
+}
+
+static int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Columns of the output that the large tile takes, the small one taking the
+// rest: all, none, or as many whole rounds of large tiles as fit, whichever
+// is estimated to end first.
+static int large_columns(int m, int k, int n, int cus) {
+    const int stages = (int)up(k, 1024) * 4;
+    const int64_t mt = up(m, kMgLargeM), nt = up(n, kMgLargeN), rounds = mt * nt / cus;
+    const int64_t whole = rounds * cus / mt * kMgLargeN;   // columns of the whole rounds
+    auto small = [&](int64_t cols) { return small_cost(up(up(m, kMgSmall) * up(cols, kMgSmall), cus), stages); };
+    double best = small(n);
+    int cols = 0;
+    if (rounds > 0 && whole < n && large_cost(rounds, stages) + small(n - whole) < best) {
+        best = large_cost(rounds, stages) + small(n - whole);
+        cols = (int)whole;
+    }
+    if (large_cost(up(mt * nt, cus), stages) < best) cols = n;
+    return cols;
 }
 
 }  // namespace bqm
@@ -181,6 +319,18 @@ extern "C" int bqm_mxfp4_gemm(const uint8_t *w, const uint8_t *ws, const uint8_t
     if (m < 1 || k < 32 || n < 1) return BQM_EINVAL;
     if (k % 32 != 0 || !aligned(w, 16) || !aligned(xq, 16) || !aligned(y, 4)) return BQM_EUNSUPPORTED;
     if (k > 1 << 22) return BQM_EUNSUPPORTED;   // the rows of a tile in 31 bits
-    const MgArgs a = {w, ws, xq, xs, y, m, k, n};
-    return launch_mg<2, 4, 2, 2>(a, as_stream(stream));
+    if (up(m, kMgSmall) * up(n, kMgSmall) * 512 > 0x7FFFFFFFll) return BQM_EUNSUPPORTED;   // 32-bit tile numbers
+    hipStream_t s = as_stream(stream);
+    MgArgs a = {w, ws, xq, xs, y, n, m, k, n, 0, 0};
+    const int cols = large_columns(m, k, n, device_cus());
+    if (cols > 0) {
+        a.n = cols;
+        const int rc = launch_mg<2, 4, 3, 2>(a, s);
+        if (rc || cols == n) return rc;
+        a.w += (int64_t)cols * (k / 2);
+        a.ws += (int64_t)cols * (k / 32);
+        a.y += cols;
+        a.n = n - cols;
+    }
+    return launch_mg<2, 2, 2, 2>(a, s);
 }
