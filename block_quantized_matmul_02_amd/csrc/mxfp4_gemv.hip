@@ -90,14 +90,27 @@ __device__ __forceinline__ void three_parts(const u32x4 (&v)[2], u32x4 (&p)[3]) 
 // sixteenth token has row 15 of the three groups.
 __device__ __forceinline__ int operand_row(int i, int h) { return i < 4 ? 4 * i + h : 4 * h + 3; }
 
-// A token's sum from the lanes' results of a wave's tile (r: column 0's lane
-// plus the column): its three parts, the smallest first.
-__device__ __forceinline__ float token_sum(const float2 *r, int tok) {
-    if (tok == 15) return (r[128 + 48].y + r[64 + 48].y) + r[48].y;
-    r += (tok / 5) * 64;
-    const int i = tok % 5;
-    return i < 4 ? r[16 * i].x : (r[32].y + r[16].y) + r[0].y;
-}
+// Where a token's sum stands among the lanes' results of a wave's tile (as
+// floats, column 0): tokens 0..3 of a group in one place, its token 4 and the
+// sixteenth token in three, which are added the smallest part first.  Without
+// branches, so that the reads of several waves' results overlap.
+struct TokenSum {
+    int a, b, c;
+    bool split;
+
+    __device__ __forceinline__ explicit TokenSum(int tok) {
+        const int i = tok % 5, at = 2 * 64 * (tok / 5);
+        split = tok == 15 || i == 4;
+        a = tok == 15 ? 2 * 48 + 1 : i < 4 ? at + 2 * 16 * i : at + 1;
+        b = tok == 15 ? 2 * (64 + 48) + 1 : i < 4 ? a : a + 2 * 16;
+        c = tok == 15 ? 2 * (128 + 48) + 1 : i < 4 ? a : a + 2 * 32;
+    }
+    __device__ __forceinline__ float operator()(const float2 *r) const {
+        const float *const f = reinterpret_cast<const float *>(r);
+        const float x = f[a], y = f[b], z = f[c];
+        return split ? (z + y) + x : x;
+    }
+};
 
 // WIDE: scale rows are whole, aligned dwords (k % 128 == 0); else bytes.
 template <int G, bool WIDE>
@@ -169,7 +182,7 @@ __global__ __launch_bounds__(kMvMaxWaves * 64, G == 1 ? (WIDE ? 4 : 3) : 2) void
                 }
                 if (grp == 0) {
                     load(t0, 0);
-                    load(t1, 1);
+                    if constexpr (G < 3) load(t1, 1);
                 }
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
@@ -199,18 +212,20 @@ __global__ __launch_bounds__(kMvMaxWaves * 64, G == 1 ? (WIDE ? 4 : 3) : 2) void
         }
         __syncthreads();   // the x operands' LDS becomes the weight tiles'
 
-        auto multiply = [&](const MvTile &t, float2 *out) {
+        auto multiply = [&](MvTile &t, int next, float2 *out) {
 #pragma unroll
             for (int i = 0; i < 4; i++)
                 *reinterpret_cast<u32x4 *>(tile + (4 * i + g4) * kMvRowStride + 16 * r16) = t.c[i];
+            const unsigned sc = t.s;
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            load(t, next);
             v4f acc[G];
 #pragma unroll
             for (int grp = 0; grp < G; grp++) acc[grp] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int q = 0; q < 4; q++) {
                 const u32x4 c = *reinterpret_cast<const u32x4 *>(tile + r16 * kMvRowStride + (4 * g4 + q) * 16);
-                const float s = __builtin_bit_cast(float, ((t.s >> (8 * q)) & 255u) << 23);
+                const float s = __builtin_bit_cast(float, ((sc >> (8 * q)) & 255u) << 23);
 #pragma unroll
                 for (int d = 0; d < 4; d++) {
                     const v8bf b = eight(c[d], s);
@@ -252,21 +267,25 @@ __global__ __launch_bounds__(kMvMaxWaves * 64, G == 1 ? (WIDE ? 4 : 3) : 2) void
                     if (o < 32 * a.m && where(o, tok, col, at)) old[i] = a.y[at];
                 }
             }
-            multiply(t0, set + wave * kRed);
-            load(t0, round + 2);
-            multiply(t1, set + (waves + wave) * kRed);
-            load(t1, round + 3);
+            if constexpr (G < 3) {
+                multiply(t0, round + 2, set + wave * kRed);
+                multiply(t1, round + 3, set + (waves + wave) * kRed);
+            } else {
+                multiply(t0, round + 1, set + wave * kRed);
+                multiply(t0, round + 2, set + (waves + wave) * kRed);
+            }
             __syncthreads();
             for (int o = part * 64 + lane, i = 0; o < 32 * a.m; o += 64 * a.parts, i++) {
                 int tok, col;
                 int64_t at;
                 if (!where(o, tok, col, at)) continue;
                 const float2 *const q = set + ((o >= 16 * a.m ? waves : 0) + group * a.parts) * kRed + col;
+                const TokenSum token(tok);
                 float v[kMvMaxWaves];
 #pragma unroll
                 for (int p = 0; p < kMvMaxWaves; p++) {
                     const float2 *const r = q + (p < a.parts ? p : 0) * kRed;
-                    const float one = token_sum(r, tok);
+                    const float one = token(r);
                     v[p] = p < a.parts ? one : 0.0f;
                 }
                 float sum = v[0];
@@ -281,22 +300,24 @@ __global__ __launch_bounds__(kMvMaxWaves * 64, G == 1 ? (WIDE ? 4 : 3) : 2) void
 
 // Up to five tokens whose operand fits in LDS.  The whole workgroup cuts x once
 // into [3 m rows][k] bf16 and each step's operand is read from there (a few
-// lanes' worth), so a wave goes through any number of 512-k slices: items
-// (tile, slice) in order, kMvAhead of them loaded ahead, each slice's result
-// kept apart in LDS so that they are added in the same order as the passes
-// above add them, whatever k is.
-constexpr int kMvAhead = 4;
-
+// lanes' worth), so a wave goes through any number of 512-k slices.  An item is
+// one slice of R tiles of 16 weight rows, which share the operand and give R
+// independent chains of MFMAs; kAhead items are on their way.  Each slice's
+// result is kept apart in LDS, so that they are added as the passes above add
+// them: a token's bits do not depend on which kernel ran.
 struct MvDecode {
     MvArgs a;
     int slices;     // 512-k slices of a row
-    int per_wave;   // slices of a wave: ceil(slices / 8)
-    int batch;      // tiles between barriers
+    int parts;      // waves along k: min(slices, 8)
+    int subs;       // groups of tiles of a workgroup at a time: 8 / parts
+    int per_wave;   // slices of a wave: ceil(slices / parts)
+    int batch;      // groups of R tiles between barriers
     int two_sets;   // results have two sets in LDS; else a second barrier
 };
 
-template <bool WIDE>
-__global__ __launch_bounds__(kMvMaxWaves * 64, WIDE ? 4 : 2) void mxfp4_decode_kernel(MvDecode d) {
+template <int R, bool WIDE>
+__global__ __launch_bounds__(kMvMaxWaves * 64, R == 2 && WIDE ? 4 : 2) void mxfp4_decode_kernel(MvDecode d) {
+    constexpr int kAhead = R == 1 ? 4 : 1;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const MvArgs &a = d.a;
     const int lane = threadIdx.x & 63;
@@ -304,70 +325,83 @@ __global__ __launch_bounds__(kMvMaxWaves * 64, WIDE ? 4 : 2) void mxfp4_decode_k
     const int r16 = lane & 15, g4 = lane >> 4;
     const int nblk = a.k / 32;
     const int64_t row_bytes = a.k / 2;
-    const int tiles = (a.n + kMvRows - 1) / kMvRows;
+    const int groups = (a.n + R * kMvRows - 1) / (R * kMvRows);   // groups of R tiles
     const int xstride = d.slices * kMvSlice * 2 + 16;
 
     uint8_t *const xs = lds;
     uint8_t *const tile = lds + 3 * a.m * xstride + wave * kMvTileBytes;
     float2 *const red = reinterpret_cast<float2 *>(lds + 3 * a.m * xstride + kMvMaxWaves * kMvTileBytes);
-    const int set_size = d.batch * d.slices * 64;
+    const int set_size = d.subs * d.batch * R * d.slices * 64;
+    const int sub = wave / d.parts, wpart = wave % d.parts;   // with sub == subs: a wave without work
+    const int hop = gridDim.x * d.subs;
 
-    // item j of this wave: tile (j / per_wave) of this workgroup's, slice wave + 8 (j % per_wave)
-    int next_tile = blockIdx.x, next_s = 0;
-    MvTile t[kMvAhead];
-    auto load = [&](MvTile &q) {
-        const int64_t row0 = (int64_t)next_tile * kMvRows;
-        const int64_t rows = a.n - row0 < kMvRows ? a.n - row0 : kMvRows;   // may be <= 0: nothing is read
-        const int blk0 = (wave + kMvMaxWaves * next_s) * kMvBlocks;
+    // item j of this wave: its group j / per_wave, slice wpart + parts (j % per_wave)
+    int next_group = sub < d.subs ? blockIdx.x * d.subs + sub : groups, next_s = 0;
+    struct Item {
+        MvTile t[R];
+    };
+    Item it[kAhead];
+    auto load = [&](Item &q) {
+        const int64_t row0 = (int64_t)next_group * (R * kMvRows);
+        const int64_t rows = a.n - row0 < R * kMvRows ? a.n - row0 : R * kMvRows;   // may be <= 0: nothing is read
+        const int blk0 = (wpart + d.parts * next_s) * kMvBlocks;
         const __amdgpu_buffer_rsrc_t rw = mx_rsrc(a.w + row0 * row_bytes, rows * row_bytes);
         const __amdgpu_buffer_rsrc_t rs = mx_rsrc(a.ws + row0 * nblk, rows * nblk);
         const uint32_t off = blk0 + r16 < nblk ? (uint32_t)(g4 * row_bytes + 16 * (blk0 + r16)) : 0x80000000u;
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            q.c[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, off + (uint32_t)(4 * i * row_bytes), 0, 0));
         const int b = blk0 + 4 * g4;
-        if constexpr (WIDE) {
-            q.s = __builtin_amdgcn_raw_buffer_load_b32(rs, b < nblk ? (uint32_t)(r16 * nblk + b) : 0x80000000u, 0, 0);
-        } else {
-            q.s = 0;
 #pragma unroll
-            for (int e = 0; e < 4; e++)
-                q.s |= (unsigned)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
-                           rs, b + e < nblk ? (uint32_t)(r16 * nblk + b + e) : 0x80000000u, 0, 0) << (8 * e);
+        for (int h = 0; h < R; h++) {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                q.t[h].c[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, off + (uint32_t)((16 * h + 4 * i) * row_bytes), 0, 0));
+            if constexpr (WIDE) {
+                q.t[h].s = __builtin_amdgcn_raw_buffer_load_b32(rs, b < nblk ? (uint32_t)((16 * h + r16) * nblk + b) : 0x80000000u, 0, 0);
+            } else {
+                q.t[h].s = 0;
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    q.t[h].s |= (unsigned)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
+                                    rs, b + e < nblk ? (uint32_t)((16 * h + r16) * nblk + b + e) : 0x80000000u, 0, 0) << (8 * e);
+            }
         }
         if (++next_s == d.per_wave) {
             next_s = 0;
-            next_tile += gridDim.x;
+            next_group += hop;
         }
     };
 
     // x: eight values a thread and turn; zeros up to a whole slice
     const int per_row = d.slices * 64;
     const __amdgpu_buffer_rsrc_t rx = mx_rsrc(a.x, 4ll * a.m * a.k);
-    auto load_x = [&](int i, u32x4 (&v)[2], int &tok, int &at) {
-        tok = i / per_row;
-        at = i - tok * per_row;
+    auto load_x = [&](int i, u32x4 (&v)[2]) {
+        const int tok = i / per_row, at = i - tok * per_row;
         const uint32_t off = 8 * at < a.k ? (uint32_t)(4 * (tok * a.k + 8 * at)) : 0x80000000u;
         v[0] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, off, 0, 0));
         v[1] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, off + 16, 0, 0));
     };
-    {
-        u32x4 v[2];
-        int tok, at;
-        load_x(threadIdx.x, v, tok, at);
+    auto store_x = [&](int i, const u32x4 (&v)[2]) {
+        const int tok = i / per_row, at = i - tok * per_row;
+        u32x4 p[3];
+        three_parts(v, p);
+        if (i < a.m * per_row) {
 #pragma unroll
-        for (int i = 0; i < kMvAhead; i++) load(t[i]);
-        for (int i = threadIdx.x;;) {
-            u32x4 p[3];
-            three_parts(v, p);
-            if (i < a.m * per_row) {
-#pragma unroll
-                for (int h = 0; h < 3; h++) *reinterpret_cast<u32x4 *>(xs + (3 * tok + h) * xstride + 16 * at) = p[h];
-            }
-            i += kMvMaxWaves * 64;
-            if (i - (int)threadIdx.x >= a.m * per_row) break;
-            load_x(i, v, tok, at);
+            for (int h = 0; h < 3; h++) *reinterpret_cast<u32x4 *>(xs + (3 * tok + h) * xstride + 16 * at) = p[h];
         }
+    };
+    {
+        // the values are asked for before the first weights, all at once: what
+        // fits in LDS is at most five turns
+        constexpr int T = kMvMaxWaves * 64, kTurns = 5;
+        const int turns = (a.m * per_row + T - 1) / T;
+        u32x4 v[kTurns][2];
+#pragma unroll
+        for (int u = 0; u < kTurns; u++)
+            if (u < turns) load_x(threadIdx.x + u * T, v[u]);
+#pragma unroll
+        for (int i = 0; i < kAhead; i++) load(it[i]);
+#pragma unroll
+        for (int u = 0; u < kTurns; u++)
+            if (u < turns) store_x(threadIdx.x + u * T, v[u]);
     }
     __syncthreads();
 
@@ -376,22 +410,30 @@ __global__ __launch_bounds__(kMvMaxWaves * 64, WIDE ? 4 : 2) void mxfp4_decode_k
     const bool used = tok < a.m && r16 != 15;
     const uint8_t *const xrow = xs + (used ? 3 * tok + part : 0) * xstride + 4 * g4 * 64;
 
-    int s = 0, b = 0, first = blockIdx.x, set = 0;   // slice turn, tile of the batch, the batch's first tile
-    const int mine = (tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x * d.per_wave;
-    auto item = [&](MvTile &q, int j) {
+    int s = 0, b = 0, first = blockIdx.x * d.subs, set = 0;   // slice turn, group of the batch, the batch's first group
+    const int mine = (groups - first + hop - 1) / hop * d.per_wave;   // items, the same for all waves
+    auto item = [&](Item &q, int j) {
+        u32x4 c[R][4];
+        unsigned sc[R];
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-            *reinterpret_cast<u32x4 *>(tile + (4 * i + g4) * kMvRowStride + 16 * r16) = q.c[i];
-        const unsigned sc = q.s;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        for (int h = 0; h < R; h++) {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                *reinterpret_cast<u32x4 *>(tile + (4 * i + g4) * kMvRowStride + 16 * r16) = q.t[h].c[i];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int i = 0; i < 4; i++) c[h][i] = *reinterpret_cast<const u32x4 *>(tile + r16 * kMvRowStride + (4 * g4 + i) * 16);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            sc[h] = q.t[h].s;
+        }
         load(q);
-        const int slice = wave + kMvMaxWaves * s;
+        const int slice = wpart + d.parts * s;
         const uint8_t *const xp = xrow + (slice < d.slices ? slice : 0) * (kMvSlice * 2);
-        v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        v4f acc[R];
+#pragma unroll
+        for (int h = 0; h < R; h++) acc[h] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int qq = 0; qq < 4; qq++) {
-            const u32x4 c = *reinterpret_cast<const u32x4 *>(tile + r16 * kMvRowStride + (4 * g4 + qq) * 16);
-            const float f = __builtin_bit_cast(float, ((sc >> (8 * qq)) & 255u) << 23);
             u32x4 xv[4];
 #pragma unroll
             for (int e = 0; e < 4; e++) {
@@ -400,63 +442,112 @@ __global__ __launch_bounds__(kMvMaxWaves * 64, WIDE ? 4 : 2) void mxfp4_decode_k
             }
 #pragma unroll
             for (int e = 0; e < 4; e++)
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, xv[e]), eight(c[e], f), acc, 0, 0, 0);
+#pragma unroll
+                for (int h = 0; h < R; h++) {
+                    const float f = __builtin_bit_cast(float, ((sc[h] >> (8 * qq)) & 255u) << 23);
+                    acc[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, xv[e]), eight(c[h][qq][e], f), acc[h], 0, 0, 0);
+                }
         }
-        if (slice < d.slices)
-            red[set * set_size + (b * d.slices + slice) * 64 + lane] = make_float2((acc[2] + acc[1]) + acc[0], acc[3]);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (slice < d.slices && sub < d.subs) {
+#pragma unroll
+            for (int h = 0; h < R; h++)
+                red[set * set_size + (((b * d.subs + sub) * R + h) * d.slices + slice) * 64 + lane] = make_float2((acc[h][2] + acc[h][1]) + acc[h][0], acc[h][3]);
+        }
         if (++s < d.per_wave) return;
         s = 0;
         if (++b < d.batch && j + 1 < mine) return;
         __syncthreads();
-        for (int o = threadIdx.x; o < 16 * a.m * b; o += kMvMaxWaves * 64) {
-            const int col = o & 15, tk = (o >> 4) % a.m, tl = (o >> 4) / a.m;
-            const int64_t row = ((int64_t)first + (int64_t)tl * gridDim.x) * kMvRows + col;
+        // A pass's waves are added in wave order, then the passes.  With more
+        // than one pass, four lanes share an output, a pass each in turn, and
+        // the first adds what they find.
+        const int per = d.slices > a.parts ? 4 : 1;
+        for (int o = threadIdx.x; o < 16 * R * a.m * b * d.subs * per; o += kMvMaxWaves * 64) {
+            const int col = o & 15, unit = (o >> 4) / per, lead = per == 1 ? 0 : (o >> 4) & 3;
+            const int tk = unit % a.m, tl = unit / a.m, gr = tl / R;   // group gr % subs of the batch's gr / subs
+            const int64_t row = (((int64_t)first + (int64_t)(gr / d.subs) * hop + gr % d.subs) * R + tl % R) * kMvRows + col;
             const float2 *r = red + set * set_size + tl * d.slices * 64 + col;
-            float y = 0.0f;
-            for (int p0 = 0; p0 < d.slices; p0 += a.parts) {
-                float sum = token_sum(r + p0 * 64, tk);
-                for (int p = 1; p < a.parts && p0 + p < d.slices; p++) sum += token_sum(r + (p0 + p) * 64, tk);
-                y = p0 == 0 ? sum : y + sum;
+            const TokenSum token(tk);
+            auto pass_sum = [&](int p0) {
+                float v[kMvMaxWaves];
+#pragma unroll
+                for (int p = 0; p < kMvMaxWaves; p++) {
+                    const bool in = p < a.parts && p0 + p < d.slices;
+                    const float one = token(r + (in ? p0 + p : 0) * 64);
+                    v[p] = in ? one : 0.0f;
+                }
+                float sum = v[0];
+#pragma unroll
+                for (int p = 1; p < kMvMaxWaves; p++) sum += v[p];
+                return sum;
+            };
+            float y = pass_sum(lead * a.parts);
+            if (per == 4) {
+                // 16 outputs x 4 lanes are a wave's, whole (16 R m b subs per is a multiple of 64)
+                const int src = lane & 15;
+                float all = 0.0f;
+                for (int p0 = 0; p0 < a.passes; p0 += 4) {
+                    const float mine_sum = p0 == 0 ? y : pass_sum((p0 + lead) * a.parts);
+#pragma unroll
+                    for (int q = 0; q < 4; q++) {
+                        const float one = __shfl(mine_sum, src + 16 * q);
+                        if (p0 + q < a.passes) all = p0 + q == 0 ? one : all + one;
+                    }
+                }
+                y = all;
             }
-            if (row < a.n) a.y[(int64_t)tk * a.n + row] = y;
+            if (row < a.n && lead == 0) a.y[(int64_t)tk * a.n + row] = y;
         }
         b = 0;
-        first += d.batch * gridDim.x;
+        first += d.batch * hop;
         if (d.two_sets)
             set ^= 1;
         else
             __syncthreads();
     };
 #pragma unroll 1
-    for (int j = 0; j < mine; j += kMvAhead) {
-        item(t[0], j);
-        if (j + 1 < mine) item(t[1], j + 1);
-        if (j + 2 < mine) item(t[2], j + 2);
-        if (j + 3 < mine) item(t[3], j + 3);
+    for (int j = 0; j < mine; j += kAhead) {
+        item(it[0], j);
+        if constexpr (kAhead == 4) {
+            if (j + 1 < mine) item(it[1], j + 1);
+            if (j + 2 < mine) item(it[2], j + 2);
+            if (j + 3 < mine) item(it[3], j + 3);
+        }
     }
 }
 
-template <bool WIDE>
-static int launch_decode(MvDecode d, int cus, hipStream_t s) {
+// LDS of the operand and the waves' tiles.
+static int decode_lds(int m, int slices) { return 3 * m * (slices * kMvSlice * 2 + 16) + kMvMaxWaves * kMvTileBytes; }
+
+template <int R, bool WIDE>
+static int launch_decode_r(MvDecode d, int cus, hipStream_t s) {
     static LaunchCache cache;
-    const void *fn = reinterpret_cast<const void *>(&mxfp4_decode_kernel<WIDE>);
+    const void *fn = reinterpret_cast<const void *>(&mxfp4_decode_kernel<R, WIDE>);
     const int rc = raise_lds_limit(cache, fn, 160 * 1024);
     if (rc) return rc;
-    const int fixed = 3 * d.a.m * (d.slices * kMvSlice * 2 + 16) + kMvMaxWaves * kMvTileBytes;
-    const int tiles = (d.a.n + kMvRows - 1) / kMvRows;
-    const int each = (tiles + cus - 1) / cus;
-    d.per_wave = (d.slices + kMvMaxWaves - 1) / kMvMaxWaves;
-    d.batch = each < 4 ? each : 4;
-    if (d.batch > 4 / d.per_wave) d.batch = d.per_wave >= 4 ? 1 : 4 / d.per_wave;
-    const int set_bytes = d.batch * d.slices * 64 * (int)sizeof(float2);
-    d.two_sets = fixed + 2 * set_bytes <= 160 * 1024;
-    const int bytes = fixed + (d.two_sets ? 2 : 1) * set_bytes;
+    const int fixed = decode_lds(d.a.m, d.slices);
+    const int groups = (d.a.n + R * kMvRows - 1) / (R * kMvRows);
+    d.parts = d.slices < kMvMaxWaves ? d.slices : kMvMaxWaves;
+    d.subs = kMvMaxWaves / d.parts;
+    d.per_wave = (d.slices + d.parts - 1) / d.parts;
+    const int one = d.subs * R * d.slices * 64 * (int)sizeof(float2);
+    d.batch = 4 / R / d.per_wave;
+    const int units = (groups + d.subs - 1) / d.subs, each = (units + cus - 1) / cus;
+    if (d.batch > each) d.batch = each;
+    if (d.batch < 1) d.batch = 1;
+    while (d.batch > 1 && fixed + d.batch * one > 160 * 1024) d.batch--;
+    d.two_sets = fixed + 2 * d.batch * one <= 160 * 1024;
+    const int bytes = fixed + (d.two_sets ? 2 : 1) * d.batch * one;
     const int most = cus * blocks_per_cu(cache, fn, kMvMaxWaves * 64, bytes, 2);
-    const int rounds = (tiles + most - 1) / most;
-    const int grid = (tiles + rounds - 1) / rounds;
-    hipLaunchKernelGGL((mxfp4_decode_kernel<WIDE>), dim3(grid), dim3(kMvMaxWaves * 64), bytes, s, d);
+    hipLaunchKernelGGL((mxfp4_decode_kernel<R, WIDE>), dim3(units < most ? units : most), dim3(kMvMaxWaves * 64), bytes, s, d);
     return launch_status();
+}
+
+// Two tiles an item where every compute unit gets some and their results fit.
+template <bool WIDE>
+static int launch_decode(const MvDecode &d, int cus, hipStream_t s) {
+    const int one = d.slices < kMvMaxWaves ? kMvMaxWaves * 64 * 8 : d.slices * 64 * 8;   // bytes of a tile's results, at most
+    const bool fits = decode_lds(d.a.m, d.slices) + 2 * one <= 160 * 1024;
+    return fits && d.a.n >= 32 * cus ? launch_decode_r<2, WIDE>(d, cus, s) : launch_decode_r<1, WIDE>(d, cus, s);
 }
 
 template <int G, bool WIDE>
@@ -499,8 +590,8 @@ extern "C" int bqm_mxfp4_gemv(const uint8_t *w, const uint8_t *ws, const float *
     a.groups = kMvMaxWaves / a.parts;
     hipStream_t s = as_stream(stream);
     // up to five tokens: in one pass if x, the tiles and one batch's results fit in LDS
-    if (m <= 5 && (int64_t)slices * (3 * m * kMvSlice * 2 + 512) + 3 * m * 16 + kMvMaxWaves * kMvTileBytes <= 160 * 1024) {
-        const MvDecode d = {a, slices, 0, 0, 0};
+    if (m <= 5 && slices * m <= 40 && decode_lds(m, slices) + (slices < kMvMaxWaves ? kMvMaxWaves : slices) * 512 <= 160 * 1024) {
+        const MvDecode d = {a, slices, 0, 0, 0, 0, 0};
         return k % 128 == 0 && aligned(ws, 4) ? launch_decode<true>(d, device_cus(), s) : launch_decode<false>(d, device_cus(), s);
     }
     if (m <= 5) return launch_mv_scales<1>(a, s);

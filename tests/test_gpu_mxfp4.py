@@ -194,7 +194,8 @@ def test_gemm_nan_blocks_stay_in_their_row(bqm, m):
 
 GEMV = [(1, 32, 1), (1, 4096, 1000), (2, 1280, 333), (3, 96, 17), (4, 5120, 64), (5, 4096, 257), (6, 4096, 257),
         (7, 1056, 100), (9, 4096, 129), (10, 544, 77), (11, 2880, 50), (16, 4096, 96), (16, 32, 16), (1, 17408, 333),
-        (9, 17408, 40), (16, 8224, 33), (1, 512, 70000), (2, 2048, 4096)]
+        (9, 17408, 40), (16, 8224, 33), (1, 512, 70000), (2, 2048, 4096), (1, 17408, 9000), (2, 9728, 8200),
+        (5, 4096, 8300), (3, 1536, 9001), (4, 64, 9000)]
 
 
 @pytest.mark.parametrize("m,k,n", GEMV)
