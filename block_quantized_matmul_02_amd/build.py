@@ -26,7 +26,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["q8_1_quantize.hip", "q8_0_gemv.hip", "q8_0_gemv_mma.hip", "q8_0_gemm.hip", "e4m3.hip", "e4m3_exact.hip", "e4m3_gemv.hip", "f16_mirror.hip", "e4m3_blk.hip", "norm.hip",
-           "mxfp4_quantize.hip", "mxfp4_gemm.hip", "mxfp4_gemv.hip", "logprobs.hip", "strerror.cpp"]
+           "mxfp4_quantize.hip", "mxfp4_gemm.hip", "mxfp4_stream.hip", "mxfp4_gemv.hip", "logprobs.hip", "strerror.cpp"]
 
 HIPFLAGS = [
     f"--offload-arch={ARCH}",
@@ -46,6 +46,7 @@ EXTRA = {
     "q8_0_gemv_mma.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "e4m3_exact.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "e4m3_blk.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "mxfp4_stream.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "mxfp4_gemv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }
 

@@ -1,0 +1,33 @@
+// Shared by the kernels of the MXFP4 products.
+#pragma once
+
+#include "values.h"
+
+namespace bqm {
+
+struct MgArgs {
+    const uint8_t *w, *ws, *xq, *xs;
+    float *y;
+    int64_t ldy;          // floats between rows of y
+    int m, k, n;
+    int mtiles, ntiles;
+};
+
+// A buffer whose reads past `bytes` give zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t mx_rsrc(const void *base, int64_t bytes) {
+    const uint32_t b = bytes <= 0 ? 0u : bytes > 0x7FFFFFF0ll ? 0x7FFFFFF0u : (uint32_t)bytes;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)b, 0x00020000);
+}
+
+// Widest aligned loads of scale rows of `nblk` bytes: 16, 4 or 1.
+inline int scale_load(int nblk, const void *a, const void *b) {
+    if (nblk % 16 == 0 && aligned(a, 16) && aligned(b, 16)) return 16;
+    return nblk % 4 == 0 && aligned(a, 4) && aligned(b, 4) ? 4 : 1;
+}
+
+// The product for few tokens (mxfp4_stream.hip): whether it takes a shape, and
+// its launch (arguments already checked by the GEMM entry).
+bool mxfp4_stream_applies(int m, int k, int n);
+int mxfp4_stream(const MgArgs &a, hipStream_t s);
+
+}  // namespace bqm

@@ -8,7 +8,7 @@
 // they are stored: nothing is decoded and nothing folded.
 #include <type_traits>
 
-#include "values.h"
+#include "mxfp4.h"
 
 namespace bqm {
 
@@ -16,21 +16,8 @@ constexpr int kMgStage = 256;                 // k of an LDS stage: 8 scale bloc
 constexpr int kMgRowBytes = kMgStage / 2;
 constexpr int kMgSuper = 4;                   // stages whose scales are staged together: 32 bytes a row
 
-struct MgArgs {
-    const uint8_t *w, *ws, *xq, *xs;
-    float *y;
-    int64_t ldy;          // floats between rows of y
-    int m, k, n;
-    int mtiles, ntiles;
-};
-
 constexpr int kMgLargeM = 192, kMgLargeN = 256;   // the large tile: 8 waves of 96 x 64
 constexpr int kMgSmall = 128;                     // the small one: 4 waves of 64 x 64
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t mg_rsrc(const void *base, int64_t bytes) {
-    const uint32_t b = bytes <= 0 ? 0u : bytes > 0x7FFFFFF0ll ? 0x7FFFFFF0u : (uint32_t)bytes;
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)b, 0x00020000);
-}
 
 template <int Q>
 __device__ __forceinline__ v16f mg_mfma(u32x4 a, u32x4 b, v16f c, int sa, int sb) {
@@ -75,10 +62,10 @@ __global__ __launch_bounds__(64 * WM * WN) void mxfp4_gemm_kernel(MgArgs a) {
     const int supers = (nblk + 8 * kMgSuper - 1) / (8 * kMgSuper);
 
     const int64_t rowsA = a.m - m0 < BM ? a.m - m0 : BM, rowsB = a.n - n0 < BN ? a.n - n0 : BN;
-    const __amdgpu_buffer_rsrc_t rA = mg_rsrc(a.xq + m0 * rb, rowsA * rb);
-    const __amdgpu_buffer_rsrc_t rB = mg_rsrc(a.w + n0 * rb, rowsB * rb);
-    const __amdgpu_buffer_rsrc_t rSA = mg_rsrc(a.xs + m0 * nblk, rowsA * nblk);
-    const __amdgpu_buffer_rsrc_t rSB = mg_rsrc(a.ws + n0 * nblk, rowsB * nblk);
+    const __amdgpu_buffer_rsrc_t rA = mx_rsrc(a.xq + m0 * rb, rowsA * rb);
+    const __amdgpu_buffer_rsrc_t rB = mx_rsrc(a.w + n0 * rb, rowsB * rb);
+    const __amdgpu_buffer_rsrc_t rSA = mx_rsrc(a.xs + m0 * nblk, rowsA * nblk);
+    const __amdgpu_buffer_rsrc_t rSB = mx_rsrc(a.ws + n0 * nblk, rowsB * nblk);
 
     struct Regs {
         u32x4 a[CA], b[CB];
@@ -271,10 +258,10 @@ static int launch_mg(MgArgs a, hipStream_t s) {
     a.ntiles = (a.n + BN - 1) / BN;
     const int64_t grid = (int64_t)a.mtiles * a.ntiles;
     if (grid * NT > 0xFFFFFFFFll) return BQM_EUNSUPPORTED;   // the dispatch counts work items in 32 bits
-    const int nblk = a.k / 32;
-    if (nblk % 16 == 0 && aligned(a.ws, 16) && aligned(a.xs, 16))
+    const int sw = scale_load(a.k / 32, a.ws, a.xs);
+    if (sw == 16)
         hipLaunchKernelGGL((mxfp4_gemm_kernel<WM, WN, TM, TN, 16>), dim3((unsigned)grid), dim3(NT), 0, s, a);
-    else if (nblk % 4 == 0 && aligned(a.ws, 4) && aligned(a.xs, 4))
+    else if (sw == 4)
         hipLaunchKernelGGL((mxfp4_gemm_kernel<WM, WN, TM, TN, 4>), dim3((unsigned)grid), dim3(NT), 0, s, a);
     else
         hipLaunchKernelGGL((mxfp4_gemm_kernel<WM, WN, TM, TN, 1>), dim3((unsigned)grid), dim3(NT), 0, s, a);
@@ -322,6 +309,7 @@ extern "C" int bqm_mxfp4_gemm(const uint8_t *w, const uint8_t *ws, const uint8_t
     if (up(m, kMgSmall) * up(n, kMgSmall) * 512 > 0x7FFFFFFFll) return BQM_EUNSUPPORTED;   // 32-bit tile numbers
     hipStream_t s = as_stream(stream);
     MgArgs a = {w, ws, xq, xs, y, n, m, k, n, 0, 0};
+    if (mxfp4_stream_applies(m, k, n)) return mxfp4_stream(a, s);
     const int cols = large_columns(m, k, n, device_cus());
     if (cols > 0) {
         a.n = cols;

@@ -21,7 +21,7 @@
 //    blocks 4g .. 4g+3 of the 512 k, so that its four scales are one dword.
 //    The order of k inside a step is the same for x, and free.
 //  * The waves' partial tiles meet in LDS, added in wave order.
-#include "values.h"
+#include "mxfp4.h"
 
 namespace bqm {
 
@@ -50,11 +50,6 @@ struct MvTile {
     u32x4 c[4];
     unsigned s;
 };
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t mx_rsrc(const void *base, int64_t bytes) {
-    const uint32_t b = bytes <= 0 ? 0u : bytes > 0x7FFFFFF0ll ? 0x7FFFFFF0u : (uint32_t)bytes;
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)b, 0x00020000);
-}
 
 // Two codes of byte `sel` of q, scaled, as bf16.
 template <int SEL>

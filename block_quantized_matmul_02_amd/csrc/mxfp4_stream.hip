@@ -1,0 +1,265 @@
+// The MXFP4 x MXFP4 product for few tokens (up to 64, as long as their codes
+// fit in LDS): HBM-bound, every weight read once.
+//
+//  * The workgroup keeps the tokens' codes and scales in LDS, in the order in
+//    which the matrix cores take them: a lane's 16 bytes of each 16-token
+//    group and 128-k step follow the lane before's, and its four scales of 512
+//    k are one dword.
+//  * A wave streams tiles of 16 weight rows, 512 k at a time, straight from
+//    memory into the operand registers of v_mfma_scale_f32_16x16x128 (lane:
+//    row r = l % 16, block 4 i + l / 16 of step i), kAhead items ahead.
+//  * The workgroup's waves share a tile's k (`parts` of them) or take tiles
+//    of their own, as many along k as leave every wave work; parts meet in
+//    LDS, added in wave order.
+#include <type_traits>
+
+#include "mxfp4.h"
+
+namespace bqm {
+
+constexpr int kMsWaves = 8;
+constexpr int kMsMaxGroups = 4;             // of 16 tokens
+constexpr int kMsLds = 160 * 1024;
+
+struct MsArgs {
+    MgArgs a;
+    int slices;     // 512-k slices of a row
+    int parts;      // waves along k
+    int subs;       // tiles of a workgroup at a time: 8 / parts
+    int per_wave;   // slices of a wave
+};
+
+// Bytes of LDS: codes, scales, one tile's partial results.
+static int64_t ms_lds(int groups, int slices) { return (int64_t)groups * slices * (4096 + 256) + kMsWaves * 1024; }
+
+template <int Q>
+__device__ __forceinline__ v4f ms_mfma(u32x4 a, u32x4 b, v4f c, int sa, int sb) {
+    const v8i va = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+    const v8i vb = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(va, vb, c, 4, 4, Q, sa, Q, sb);
+}
+
+// G: groups of 16 tokens; SW: scale rows in aligned 16-byte pieces (16) or bytes (1).
+template <int G, int SW>
+__global__ __launch_bounds__(kMsWaves * 64, G == 1 ? 4 : 2) void mxfp4_stream_kernel(MsArgs d) {
+    constexpr int kAhead = 3;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const MgArgs &a = d.a;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r16 = lane & 15, g4 = lane >> 4;
+    const int nblk = a.k / 32;
+    const int64_t rb = a.k / 2;
+    const int tiles = (a.n + 15) / 16;
+    const int sub = wave / d.parts, wpart = wave % d.parts;   // with sub == subs: a wave without work
+    const int hop = gridDim.x * d.subs;
+
+    uint8_t *const xc = lds;                                              // [G][slices][4 steps][64 lanes][16]
+    int *const xsc = reinterpret_cast<int *>(lds + G * d.slices * 4096);  // [G][slices][64 lanes]
+    v4f *const red = reinterpret_cast<v4f *>(lds + G * d.slices * (4096 + 256));   // [waves][64 lanes]
+
+    struct Tile {
+        u32x4 c[4];
+        unsigned s[4];   // SW == 16: the row's 16 scales; else this lane's four
+    };
+    int next_tile = sub < d.subs ? blockIdx.x * d.subs + sub : tiles, next_s = 0;
+    auto load = [&](Tile &q) {
+        const int64_t row0 = (int64_t)next_tile * 16;
+        const int64_t rows = a.n - row0 < 16 ? a.n - row0 : 16;   // may be <= 0: nothing is read
+        const __amdgpu_buffer_rsrc_t rw = mx_rsrc(a.w + row0 * rb, rows * rb);
+        const __amdgpu_buffer_rsrc_t rs = mx_rsrc(a.ws + row0 * nblk, rows * nblk);
+        const int blk0 = (wpart + d.parts * next_s) * 16;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int b = blk0 + 4 * i + g4;   // blocks past the row's end are read as zeros
+            q.c[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                         rw, b < nblk ? (uint32_t)(r16 * rb + 16 * b) : 0x80000000u, 0, 0));
+        }
+        if constexpr (SW == 16) {
+            const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                rs, blk0 < nblk ? (uint32_t)(r16 * nblk + blk0) : 0x80000000u, 0, 0));
+#pragma unroll
+            for (int i = 0; i < 4; i++) q.s[i] = v[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int b = blk0 + 4 * i + g4;
+                q.s[i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, b < nblk ? (uint32_t)(r16 * nblk + b) : 0x80000000u, 0, 0);
+            }
+        }
+        if (++next_s == d.per_wave) {
+            next_s = 0;
+            next_tile += hop;
+        }
+    };
+    // this lane's four scales, one a byte
+    auto scales = [&](const Tile &t) {
+        if constexpr (SW == 16) {
+            // byte g4 of each dword
+            const unsigned sel = 0x0C0C0400u + 0x0101u * (unsigned)g4;
+            const unsigned lo = __builtin_amdgcn_perm(t.s[1], t.s[0], sel), hi = __builtin_amdgcn_perm(t.s[3], t.s[2], sel);
+            return (int)(lo | hi << 16);
+        } else {
+            return (int)(t.s[0] | t.s[1] << 8 | t.s[2] << 16 | t.s[3] << 24);
+        }
+    };
+
+    Tile it[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; i++) load(it[i]);
+
+    // The tokens' codes and scales, several loads of a thread at a time; tokens
+    // and blocks past the ends are read as zeros.
+    {
+        constexpr int U = 8;
+        const __amdgpu_buffer_rsrc_t rx = mx_rsrc(a.xq, a.m * rb), rxs = mx_rsrc(a.xs, (int64_t)a.m * nblk);
+        const int steps = G * d.slices * 4, per = d.slices * 4;   // a wave writes a step's 1 KiB
+        for (int st0 = wave; st0 < steps; st0 += U * kMsWaves) {
+            u32x4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int st = st0 + u * kMsWaves, grp = st / per, b = (st - grp * per) * 4 + g4;
+                const bool in = st < steps && b < nblk;
+                v[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                           rx, in ? (uint32_t)((16 * grp + r16) * rb + 16 * b) : 0x80000000u, 0, 0));
+            }
+#pragma unroll
+            for (int u = 0; u < U; u++)
+                if (st0 + u * kMsWaves < steps) *reinterpret_cast<u32x4 *>(xc + (st0 + u * kMsWaves) * 1024 + 16 * lane) = v[u];
+        }
+        constexpr int V = 4;
+        for (int sl0 = wave; sl0 < G * d.slices; sl0 += V * kMsWaves) {
+            unsigned v[V][4];
+#pragma unroll
+            for (int u = 0; u < V; u++) {
+                const int sl = sl0 + u * kMsWaves, grp = sl / d.slices;
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int b = 16 * (sl - grp * d.slices) + 4 * e + g4;
+                    const bool in = sl < G * d.slices && b < nblk;
+                    v[u][e] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rxs, in ? (uint32_t)((16 * grp + r16) * nblk + b) : 0x80000000u, 0, 0);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < V; u++)
+                if (sl0 + u * kMsWaves < G * d.slices)
+                    xsc[(sl0 + u * kMsWaves) * 64 + lane] = (int)(v[u][0] | v[u][1] << 8 | v[u][2] << 16 | v[u][3] << 24);
+        }
+    }
+    __syncthreads();
+
+    v4f acc[G] = {};
+    int s = 0, first = blockIdx.x * d.subs;   // slice turn, the workgroup's current first tile
+    const int mine = (tiles - first + hop - 1) / hop * d.per_wave;   // items, the same for all waves
+    auto item = [&](Tile &q) {
+        // a tile's first slice starts from zero (a select: no branch splits the
+        // accumulators' lifetime)
+        const float keep = s == 0 ? 0.0f : 1.0f;
+#pragma unroll
+        for (int grp = 0; grp < G; grp++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) acc[grp][e] = keep != 0.0f ? acc[grp][e] : 0.0f;
+        const int slice = wpart + d.parts * s;
+        const int at = slice < d.slices ? slice : 0;   // past the end: zero weights
+        const int sb = scales(q);
+#pragma unroll
+        for (int grp = 0; grp < G; grp++) {
+            const int sa = xsc[(grp * d.slices + at) * 64 + lane];
+            const uint8_t *const p = xc + (grp * d.slices + at) * 4096 + 16 * lane;
+            auto step = [&](auto qq) {
+                constexpr int Q = decltype(qq)::value;
+                const u32x4 x = *reinterpret_cast<const u32x4 *>(p + Q * 1024);
+                acc[grp] = ms_mfma<Q>(x, q.c[Q], acc[grp], sa, sb);
+            };
+            step(std::integral_constant<int, 0>{});
+            step(std::integral_constant<int, 1>{});
+            step(std::integral_constant<int, 2>{});
+            step(std::integral_constant<int, 3>{});
+        }
+        load(q);
+        if (++s < d.per_wave) return;
+        s = 0;
+        // lane: weight row r16, tokens 4 g4 + v of each group
+#pragma unroll
+        for (int grp = 0; grp < G; grp++) {
+            if (d.parts > 1) {
+                red[wave * 64 + lane] = acc[grp];
+                __syncthreads();
+                if (wpart == 0 && sub < d.subs) {
+                    const v4f *const q0 = red + sub * d.parts * 64 + lane;
+                    v4f v[kMsWaves];
+#pragma unroll
+                    for (int p = 0; p < kMsWaves; p++) v[p] = q0[(p < d.parts ? p : 0) * 64];
+#pragma unroll
+                    for (int p = 1; p < kMsWaves; p++)
+                        if (p < d.parts) v[0] += v[p];
+                    acc[grp] = v[0];
+                }
+                __syncthreads();
+            }
+            if (wpart == 0 && sub < d.subs) {
+                const int64_t row = (int64_t)(first + sub) * 16 + r16;
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    if (row < a.n && 16 * grp + 4 * g4 + e < a.m) a.y[(16 * grp + 4 * g4 + e) * a.ldy + row] = acc[grp][e];
+            }
+        }
+        first += hop;
+    };
+#pragma unroll 1
+    for (int j = 0; j < mine; j += kAhead) {
+        item(it[0]);
+        if (j + 1 < mine) item(it[1]);
+        if constexpr (kAhead == 3) {
+            if (j + 2 < mine) item(it[2]);
+        }
+    }
+}
+
+template <int G, int SW>
+static int launch_ms(MsArgs d, int cus, hipStream_t s) {
+    static LaunchCache cache;
+    const void *fn = reinterpret_cast<const void *>(&mxfp4_stream_kernel<G, SW>);
+    const int rc = raise_lds_limit(cache, fn, kMsLds);
+    if (rc) return rc;
+    const int tiles = (d.a.n + 15) / 16;
+    d.slices = (d.a.k + 511) / 512;
+    // waves along k: all of them, unless there are tiles enough for every wave
+    d.parts = d.slices < kMsWaves ? d.slices : kMsWaves;
+    while (d.parts > 1 && tiles >= 2 * cus * (2 * kMsWaves / d.parts)) d.parts = (d.parts + 1) / 2;
+    d.subs = kMsWaves / d.parts;
+    d.per_wave = (d.slices + d.parts - 1) / d.parts;
+    const int bytes = (int)ms_lds(G, d.slices);
+    const int units = (tiles + d.subs - 1) / d.subs;
+    const int most = cus * blocks_per_cu(cache, fn, kMsWaves * 64, bytes, 2);
+    hipLaunchKernelGGL((mxfp4_stream_kernel<G, SW>), dim3(units < most ? units : most), dim3(kMsWaves * 64), bytes, s, d);
+    return launch_status();
+}
+
+template <int G>
+static int launch_ms_g(const MgArgs &a, hipStream_t s) {
+    const MsArgs d = {a, 0, 0, 0, 0};
+    const int cus = device_cus();
+    const bool wide = scale_load(a.k / 32, a.ws, a.ws) == 16;
+    return wide ? launch_ms<G, 16>(d, cus, s) : launch_ms<G, 1>(d, cus, s);
+}
+
+// Few tokens whose operand fits in LDS, against few enough rows that the large
+// kernel's 128-row tiles would leave half of the compute units idle (there
+// it takes 16.8 us where this takes 11.5: 16 x 4096 x 5152; with more rows it
+// is ahead, 19.7 to 29 at 64 x 4096 x 20480).
+bool mxfp4_stream_applies(int m, int k, int n) {
+    const int groups = (m + 15) / 16;
+    return groups <= kMsMaxGroups && n <= 64 * device_cus() && ms_lds(groups, (int)(((int64_t)k + 511) / 512)) <= kMsLds;
+}
+
+int mxfp4_stream(const MgArgs &a, hipStream_t s) {
+    switch ((a.m + 15) / 16) {
+        case 1: return launch_ms_g<1>(a, s);
+        case 2: return launch_ms_g<2>(a, s);
+        case 3: return launch_ms_g<3>(a, s);
+        default: return launch_ms_g<4>(a, s);
+    }
+}
+
+}  // namespace bqm
