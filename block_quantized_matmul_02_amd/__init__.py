@@ -10,6 +10,7 @@ synchronize.  There is no CPU fallback: a missing library raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -28,6 +29,7 @@ BQM_F16 = 1
 BQM_BF16 = 2
 
 _lib = None
+_raw_stream = None
 
 
 class BqmError(RuntimeError):
@@ -89,12 +91,19 @@ def strerror(rc: int) -> str:
 
 
 def _stream(t):
-    import torch
+    """The handle of torch's current stream on t's device, without building a Stream object where torch allows."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
 
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _raw_stream(t.device.index)
 
 
 def _check(t, dtype, name, shape=None):
+    if t.is_cuda and t.dtype == dtype and t.is_contiguous() and (shape is None or t.shape == shape):
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if t.dtype != dtype:
@@ -106,7 +115,7 @@ def _check(t, dtype, name, shape=None):
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _raise(fn, rc):
@@ -352,10 +361,15 @@ def bqm_e4m3_blk_gemm(w, grid, xq, xs, y=None):
 # ------------------------------------------- the operators around the matmul
 
 
-def _type(t, name):
-    import torch
+_types = {}
 
-    code = {torch.float32: BQM_F32, torch.float16: BQM_F16, torch.bfloat16: BQM_BF16}.get(t.dtype)
+
+def _type(t, name):
+    if not _types:
+        import torch
+
+        _types.update({torch.float32: BQM_F32, torch.float16: BQM_F16, torch.bfloat16: BQM_BF16})
+    code = _types.get(t.dtype)
     if code is None:
         raise ValueError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
     return code
@@ -363,6 +377,10 @@ def _type(t, name):
 
 def _rows(t, name, dtype=None, shape=None):
     """Checks a 2-D GPU tensor whose rows are contiguous; returns its row stride."""
+    if t.is_cuda and (dtype is None or t.dtype == dtype) and (t.shape == shape if shape is not None else t.dim() == 2):
+        row, column = t.stride()
+        if column == 1:
+            return row
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if dtype is not None and t.dtype != dtype:
@@ -375,7 +393,7 @@ def _rows(t, name, dtype=None, shape=None):
 
 
 def _optr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _norm_args(x, res, gain, h):
@@ -519,6 +537,7 @@ def bqm_mxfp4_gemv(w, ws, x, y=None):
     return y
 
 
+@functools.lru_cache(maxsize=256)
 def bqm_logprobs_workspace(m: int, n: int, top_k: int) -> int:
     """Bytes of workspace that :func:`bqm_logprobs` needs for ``m`` rows of ``n`` logits."""
     size = lib().bqm_logprobs_workspace(m, n, top_k)
