@@ -7,29 +7,37 @@
 //
 // HBM-bound: x and res are read once and h and y written once, so a row stays
 // in registers between the sum of squares and the scaling.
-//  * A row is cut into pieces of four values; thread i of the row's NT owns
-//    pieces i, i + NT, ... (four of them).  A wave has a row of k <= 1024 to
-//    itself (no barrier); otherwise a workgroup of k/16 threads, rounded up
-//    to whole waves, has it (k <= 16384); beyond that the workgroup reads the
-//    row twice, the second time mostly from its L2.
-//  * The sum of squares is one fma chain per thread (16 values), a DPP tree
-//    over the wave, then the waves' sums in order: f32, the order a function
-//    of k alone, so a token's norm is the same bits in decode and in prefill.
-//  * A 32-value block is 8 neighbouring lanes and a 128-value block 32 of
-//    them, so the block maxima are DPP steps on values already in registers.
-//  * ALN: rows aligned to four elements move in 16-byte (f32) or 8-byte
-//    pieces; otherwise the same pieces move element by element, with the same
-//    arithmetic, for odd k and odd strides.
+//  * A row is cut into pieces of 16 bytes (four f32 or eight 16-bit values);
+//    thread i of the row's NT owns pieces i, i + NT, ... (kNormPieces of them).
+//    A wave has a row of up to 128 pieces to itself (no barrier); otherwise a
+//    workgroup, as many whole waves as the row needs, has it (up to 2048
+//    pieces); beyond that the workgroup reads the row twice, the second time
+//    mostly from its L2.  Two pieces per thread, measured against one and four
+//    at 8192 x 5120 bf16 -> e4m3 (56.9, 65.5, 65.7 us; 5.2 TB/s) and at
+//    64 x 8192 (5.1, 4.6, 6.9 us): more waves on a row shorten its chain of
+//    load, sum, barrier and store, fewer leave each enough loads in flight.
+//  * The sum of squares is one fma chain per thread, a DPP tree over the wave,
+//    then the waves' sums in order: f32, the order a function of k and the type
+//    alone, so a token's norm is the same bits in decode and in prefill.
+//  * The lanes of a 32- or 128-value block are neighbours in a row of 16 or 32
+//    lanes, so the block maxima are DPP steps on values already in registers.
+//  * The q8_1 rule rounds the correctly rounded quotient x / d.  Here the
+//    product with an approximate reciprocal decides wherever it is further
+//    from a half than its error, and only a wave that holds a value nearer
+//    than that divides: the quants are the same, for a tenth of the divisions.
+//  * ALN: rows aligned to a piece move in 16-byte accesses; otherwise the same
+//    pieces move element by element, with the same arithmetic, for odd k and
+//    odd strides.
+//  * Everything is stored past the caches: each output is larger than they are
+//    by the time it is read, where time counts.
 #include "values.h"
 
 namespace bqm {
 
 enum { kOutF32, kOutSame, kOutQ81, kOutE4m3 };
 
-constexpr int kNormPieces = 4;          // pieces of four values per thread
+constexpr int kNormPieces = 2;          // pieces per thread
 constexpr int kNormMaxThreads = 1024;
-constexpr int kNormWaveK = 64 * 4 * kNormPieces;
-constexpr int kNormRegK = kNormMaxThreads * 4 * kNormPieces;
 constexpr int kNormMaxGrid = 1 << 20;   // rows beyond it are taken in turn
 constexpr int kNormMaxK = 1 << 30;      // 32-bit positions within a row
 
@@ -43,65 +51,133 @@ struct NormArgs {
     int m, k;
 };
 
-template <typename T, bool ALN>
-__device__ __forceinline__ v4f load4(const T *p, int i, int k) {
-    v4f v = {0.0f, 0.0f, 0.0f, 0.0f};
+// A piece of T: W values.
+template <typename T>
+struct Piece {
+    static constexpr int W = 16 / sizeof(T);
+    typedef float f __attribute__((ext_vector_type(W)));
+};
+
+template <typename T, int W, bool ALN>
+__device__ __forceinline__ auto load_piece(const T *p, int i, int k) {
+    typedef float f __attribute__((ext_vector_type(W)));
+    typedef T tv __attribute__((ext_vector_type(W)));
+    f v = {};
     if constexpr (ALN) {
-        if (i < k) v = __builtin_convertvector(*reinterpret_cast<const typename Vec<T>::x4 *>(p + i), v4f);
+        if (i < k) v = __builtin_convertvector(*reinterpret_cast<const tv *>(p + i), f);
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; e++)
+        for (int e = 0; e < W; e++)
             if (i + e < k) v[e] = (float)p[i + e];
     }
     return v;
 }
 
-template <typename T, bool ALN>
-__device__ __forceinline__ void store4(T *p, int i, int k, v4f v) {
+template <typename T, int W, bool ALN, typename F>
+__device__ __forceinline__ void store_piece(T *p, int i, int k, F v) {
+    typedef T tv __attribute__((ext_vector_type(W)));
     if constexpr (ALN) {
-        if (i < k) *reinterpret_cast<typename Vec<T>::x4 *>(p + i) = __builtin_convertvector(v, typename Vec<T>::x4);
+        if (i < k) __builtin_nontemporal_store(__builtin_convertvector(v, tv), reinterpret_cast<tv *>(p + i));
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; e++)
+        for (int e = 0; e < W; e++)
             if (i + e < k) p[i + e] = (T)v[e];
     }
 }
 
 __device__ __forceinline__ float clamp448n(float v) { return fminf(fmaxf(v, -448.0f), 448.0f); }
 
-// One piece of y: values i .. i+3 of row t.  Every lane of the wave takes
+// Largest magnitude over groups of LANES neighbouring lanes, on every lane.
+template <int LANES>
+__device__ __forceinline__ float group_absmax(float v) {
+    v = fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0xB1, 0xF, 0xF, false)));
+    v = fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x4E, 0xF, 0xF, false)));
+    if constexpr (LANES >= 8)
+        v = fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x141, 0xF, 0xF, false)));
+    if constexpr (LANES >= 16)
+        v = fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x140, 0xF, 0xF, false)));
+    if constexpr (LANES >= 32) v = swap16_max(v);
+    return v;
+}
+
+// One piece of y: values i .. i+W-1 of row t.  Every lane of the wave takes
 // part (block maxima); lanes past k hold zeros and store nothing.
-template <typename T, int OUT, bool ALN>
-__device__ __forceinline__ void emit(const NormArgs &a, int64_t t, int i, v4f y) {
+template <typename T, int OUT, bool ALN, typename F>
+__device__ __forceinline__ void emit(const NormArgs &a, int64_t t, int i, F y) {
+    constexpr int W = Piece<T>::W;
+    typedef int words __attribute__((ext_vector_type(W / 4)));
     const int64_t at = t * a.k;
     if constexpr (OUT == kOutF32) {
-        store4<float, ALN>(static_cast<float *>(a.y) + at, i, a.k, y);
-    } else if constexpr (OUT == kOutSame) {
-        store4<T, ALN>(static_cast<T *>(a.y) + at, i, a.k, y);
-    } else if constexpr (OUT == kOutQ81) {
-        const Q81Lane r = q8_1_block_lane(make_float4(y[0], y[1], y[2], y[3]));
-        int sum = r.qsum;
+        store_piece<float, W, ALN>(static_cast<float *>(a.y) + at, i, a.k, y);
+        return;
+    }
+    if constexpr (OUT == kOutSame) {
+        store_piece<T, W, ALN>(static_cast<T *>(a.y) + at, i, a.k, y);
+        return;
+    }
+    float big = 0.0f;
+#pragma unroll
+    for (int e = 0; e < W; e++) big = fmaxf(big, fabsf(y[e]));
+    words q;
+    if constexpr (OUT == kOutQ81) {
+        big = group_absmax<32 / W>(big);
+        const float d = big / 127.0f;
+        const bool nz = d > 0.0f;
+        const float inv = __builtin_amdgcn_rcpf(d);
+        // |y * inv| is within 127 * 3 * 2^-24 < 2.4e-5 of the quotient, and the
+        // correctly rounded one within 7.6e-6; a tiny d has no reciprocal
+        bool near = !(d > 1e-30f) && nz;
+        float r[W];
+#pragma unroll
+        for (int e = 0; e < W; e++) {
+            const float v = fabsf(y[e] * inv);
+            const float whole = floorf(v);
+            near |= !(fabsf(v - whole - 0.5f) > 1e-4f) && nz;   // a NaN too
+            r[e] = copysignf(fminf(floorf(v + 0.5f), 127.0f), y[e]);
+        }
+        if (__ballot(near) != 0) {
+#pragma unroll
+            for (int e = 0; e < W; e++) r[e] = (float)q8_1_quant1(y[e], d, nz);
+        }
+        int sum = 0;
+#pragma unroll
+        for (int w = 0; w < W / 4; w++) {
+            unsigned b = 0;
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const int one = nz ? (int)r[4 * w + e] : 0;
+                sum += one;
+                b |= (unsigned)(one & 0xFF) << (8 * e);
+            }
+            q[w] = (int)b;
+        }
         sum += __builtin_amdgcn_update_dpp(0, sum, 0xB1, 0xF, 0xF, false);
         sum += __builtin_amdgcn_update_dpp(0, sum, 0x4E, 0xF, 0xF, false);
-        sum += __builtin_amdgcn_update_dpp(0, sum, 0x141, 0xF, 0xF, false);
-        if (i < a.k) {
-            static_cast<unsigned *>(a.y)[(at + i) >> 2] = r.packed;
-            if ((threadIdx.x & 7) == 0)
-                reinterpret_cast<float2 *>(a.scale)[(at + i) >> 5] = make_float2(r.d, r.d * (float)sum);
-        }
+        if constexpr (W == 4) sum += __builtin_amdgcn_update_dpp(0, sum, 0x141, 0xF, 0xF, false);
+        if (i < a.k && (threadIdx.x & (32 / W - 1)) == 0)
+            reinterpret_cast<float2 *>(a.scale)[(at + i) >> 5] = make_float2(d, d * (float)sum);
     } else {
-        float big = fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3])));
-        big = swap16_max(dpp_absmax16(big));
+        big = group_absmax<128 / W>(big);
         float mul = 0.0f, s = 0.0f;
         if (big > 0.0f) {
             mul = 448.0f / big;
             s = big / 448.0f;
         }
-        const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448n(y[0] * mul), clamp448n(y[1] * mul), 0, false);
-        const int q = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448n(y[2] * mul), clamp448n(y[3] * mul), lo, true);
-        if (i < a.k) {
-            static_cast<int *>(a.y)[(at + i) >> 2] = q;
-            if ((threadIdx.x & 31) == 0) a.scale[t * ((a.k + 127) >> 7) + (i >> 7)] = s;
+#pragma unroll
+        for (int w = 0; w < W / 4; w++) {
+            const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448n(y[4 * w] * mul), clamp448n(y[4 * w + 1] * mul), 0, false);
+            q[w] = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448n(y[4 * w + 2] * mul), clamp448n(y[4 * w + 3] * mul), lo, true);
+        }
+        if (i < a.k && (threadIdx.x & (128 / W - 1)) == 0) a.scale[t * ((a.k + 127) >> 7) + (i >> 7)] = s;
+    }
+    // codes: k and so every piece's place is a multiple of W (k % 16 == 0)
+    if (i < a.k) {
+        int *const p = reinterpret_cast<int *>(static_cast<uint8_t *>(a.y) + at + i);
+        if constexpr (ALN) {
+            __builtin_nontemporal_store(q, reinterpret_cast<words *>(p));
+        } else {
+#pragma unroll
+            for (int w = 0; w < W / 4; w++) p[w] = q[w];
         }
     }
 }
@@ -120,9 +196,10 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
 
 __device__ __forceinline__ float inv_rms(float sum, int k, float eps) { return 1.0f / sqrtf(sum / (float)k + eps); }
 
-__device__ __forceinline__ float squares(v4f v, float acc) {
+template <int W, typename F>
+__device__ __forceinline__ float squares(F v, float acc) {
 #pragma unroll
-    for (int e = 0; e < 4; e++) acc = __builtin_fmaf(v[e], v[e], acc);
+    for (int e = 0; e < W; e++) acc = __builtin_fmaf(v[e], v[e], acc);
     return acc;
 }
 
@@ -130,6 +207,8 @@ __device__ __forceinline__ float squares(v4f v, float acc) {
 // than the registers hold and is read twice.
 template <typename T, int OUT, bool ALN, bool WAVE, bool LONG>
 __global__ __launch_bounds__(WAVE ? 256 : kNormMaxThreads) void norm_kernel(NormArgs a) {
+    constexpr int W = Piece<T>::W;
+    typedef typename Piece<T>::f F;
     __shared__ float red[2][kNormMaxThreads / 64];
     const int lane = WAVE ? threadIdx.x & 63 : threadIdx.x;
     const int nt = WAVE ? 64 : blockDim.x;
@@ -141,45 +220,58 @@ __global__ __launch_bounds__(WAVE ? 256 : kNormMaxThreads) void norm_kernel(Norm
         T *h = static_cast<T *>(a.h) + t * a.ldh;
         float acc = 0.0f;
         if constexpr (!LONG) {
-            v4f s[kNormPieces], g[kNormPieces];
+            F s[kNormPieces];
 #pragma unroll
-            for (int c = 0; c < kNormPieces; c++) s[c] = load4<T, ALN>(x, 4 * (lane + c * nt), a.k);
+            for (int c = 0; c < kNormPieces; c++) s[c] = load_piece<T, W, ALN>(x, W * (lane + c * nt), a.k);
             if (res) {
-                v4f r[kNormPieces];
+                F r[kNormPieces];
 #pragma unroll
-                for (int c = 0; c < kNormPieces; c++) r[c] = load4<T, ALN>(res, 4 * (lane + c * nt), a.k);
+                for (int c = 0; c < kNormPieces; c++) r[c] = load_piece<T, W, ALN>(res, W * (lane + c * nt), a.k);
 #pragma unroll
                 for (int c = 0; c < kNormPieces; c++) s[c] += r[c];
             }
+            // f32: the gain is on its way during the sum (16-bit pieces have twice
+            // the values, and the registers go to more rows in flight)
+            F g[W == 4 ? kNormPieces : 1];
+            auto load_gain = [&](int c) {
+                F v = F(1.0f);
+                if (a.gain) v = load_piece<float, W, ALN>(a.gain, W * (lane + c * nt), a.k);
+                return v;
+            };
+            if constexpr (W == 4) {
 #pragma unroll
-            for (int c = 0; c < kNormPieces; c++)
-                g[c] = a.gain ? load4<float, ALN>(a.gain, 4 * (lane + c * nt), a.k) : v4f{1.0f, 1.0f, 1.0f, 1.0f};
+                for (int c = 0; c < kNormPieces; c++) g[c] = load_gain(c);
+            }
 #pragma unroll
-            for (int c = 0; c < kNormPieces; c++) acc = squares(s[c], acc);
+            for (int c = 0; c < kNormPieces; c++) acc = squares<W>(s[c], acc);
             if (res) {
 #pragma unroll
-                for (int c = 0; c < kNormPieces; c++) store4<T, ALN>(h, 4 * (lane + c * nt), a.k, s[c]);
+                for (int c = 0; c < kNormPieces; c++) store_piece<T, W, ALN>(h, W * (lane + c * nt), a.k, s[c]);
             }
             const float inv = inv_rms(WAVE ? wave_sum(acc) : block_sum(acc, red[turn]), a.k, a.eps);
 #pragma unroll
             for (int c = 0; c < kNormPieces; c++) {
-                if (4 * c * nt < a.k) emit<T, OUT, ALN>(a, t, 4 * (lane + c * nt), s[c] * inv * g[c]);
+                if (W * c * nt < a.k) {
+                    if constexpr (W != 4) g[0] = load_gain(c);
+                    emit<T, OUT, ALN>(a, t, W * (lane + c * nt), s[c] * inv * g[W == 4 ? c : 0]);
+                }
             }
         } else {
-            for (int i = 4 * lane; i - 4 * lane < a.k; i += 4 * nt) {
-                v4f s = load4<T, ALN>(x, i, a.k);
-                if (res) s += load4<T, ALN>(res, i, a.k);
-                acc = squares(s, acc);
+            for (int i = W * lane; i - W * lane < a.k; i += W * nt) {
+                F s = load_piece<T, W, ALN>(x, i, a.k);
+                if (res) s += load_piece<T, W, ALN>(res, i, a.k);
+                acc = squares<W>(s, acc);
             }
             const float inv = inv_rms(block_sum(acc, red[turn]), a.k, a.eps);
             // h may be x or res: each value is read and then written by one thread
-            for (int i = 4 * lane; i - 4 * lane < a.k; i += 4 * nt) {
-                v4f s = load4<T, ALN>(x, i, a.k);
+            for (int i = W * lane; i - W * lane < a.k; i += W * nt) {
+                F s = load_piece<T, W, ALN>(x, i, a.k);
                 if (res) {
-                    s += load4<T, ALN>(res, i, a.k);
-                    store4<T, ALN>(h, i, a.k, s);
+                    s += load_piece<T, W, ALN>(res, i, a.k);
+                    store_piece<T, W, ALN>(h, i, a.k, s);
                 }
-                const v4f g = a.gain ? load4<float, ALN>(a.gain, i, a.k) : v4f{1.0f, 1.0f, 1.0f, 1.0f};
+                F g = F(1.0f);
+                if (a.gain) g = load_piece<float, W, ALN>(a.gain, i, a.k);
                 emit<T, OUT, ALN>(a, t, i, s * inv * g);
             }
         }
@@ -188,16 +280,17 @@ __global__ __launch_bounds__(WAVE ? 256 : kNormMaxThreads) void norm_kernel(Norm
 
 template <typename T, int OUT, bool ALN>
 static int launch_norm(const NormArgs &a, hipStream_t s) {
+    constexpr int kWaveK = 64 * Piece<T>::W * kNormPieces;   // a wave's row at most
     const int64_t rows = a.m;
-    if (a.k <= kNormWaveK) {
+    if (a.k <= kWaveK) {
         const int64_t grid = (rows + 3) / 4;
         hipLaunchKernelGGL((norm_kernel<T, OUT, ALN, true, false>), dim3((unsigned)(grid < kNormMaxGrid ? grid : kNormMaxGrid)),
                            dim3(256), 0, s, a);
         return launch_status();
     }
     const unsigned grid = (unsigned)(rows < kNormMaxGrid ? rows : kNormMaxGrid);
-    if (a.k <= kNormRegK) {
-        const int nt = (a.k + 64 * 4 * kNormPieces - 1) / (64 * 4 * kNormPieces) * 64;
+    if (a.k <= kWaveK * (kNormMaxThreads / 64)) {
+        const int nt = (a.k + kWaveK - 1) / kWaveK * 64;
         hipLaunchKernelGGL((norm_kernel<T, OUT, ALN, false, false>), dim3(grid), dim3(nt), 0, s, a);
     } else {
         hipLaunchKernelGGL((norm_kernel<T, OUT, ALN, false, true>), dim3(grid), dim3(kNormMaxThreads), 0, s, a);
@@ -207,10 +300,10 @@ static int launch_norm(const NormArgs &a, hipStream_t s) {
 
 template <typename T, int OUT>
 static int launch_aligned(const NormArgs &a, hipStream_t s) {
-    const uintptr_t in = 4 * sizeof(T);
-    const uintptr_t out = OUT == kOutF32 ? 16 : OUT == kOutSame ? in : 1;
-    const bool rows4 = a.m == 1 || (a.ldx % 4 == 0 && (!a.res || (a.ldr % 4 == 0 && a.ldh % 4 == 0)));
-    const bool aln = a.k % 4 == 0 && rows4 && aligned(a.x, in) && aligned(a.res, in) && aligned(a.h, in) &&
+    constexpr int W = Piece<T>::W;
+    const uintptr_t out = OUT == kOutF32 || OUT == kOutSame ? 16 : W;
+    const bool rows = a.m == 1 || (a.ldx % W == 0 && (!a.res || (a.ldr % W == 0 && a.ldh % W == 0)));
+    const bool aln = a.k % W == 0 && rows && aligned(a.x, 16) && aligned(a.res, 16) && aligned(a.h, 16) &&
                      aligned(a.gain, 16) && aligned(a.y, out);
     return aln ? launch_norm<T, OUT, true>(a, s) : launch_norm<T, OUT, false>(a, s);
 }

@@ -53,10 +53,10 @@ extern "C" {
  *   y        : y_type [m][k] out, dense; y_type is BQM_F32 or x_type (else
  *              BQM_EUNSUPPORTED).
  *   m, k >= 1 (else BQM_EINVAL), any k.  Every pointer is aligned to its
- *   element (else BQM_EUNSUPPORTED); rows that are aligned to four elements
- *   take wide loads.  Strides are unused when m is 1.
- * The order of the sums depends on k alone: a row's result does not depend
- * on m, on the strides or on the alignment.
+ *   element (else BQM_EUNSUPPORTED); rows that are aligned to 16 bytes take
+ *   wide loads.  Strides are unused when m is 1.
+ * The order of the sums depends on k and x_type alone: a row's result does
+ * not depend on m, on the strides or on the alignment.
  */
 int bqm_add_rmsnorm(const void *x, int64_t ldx, const void *res, int64_t ldr, const float *gain, float eps, void *h,
                     int64_t ldh, void *y, int x_type, int y_type, int m, int k, void *stream);

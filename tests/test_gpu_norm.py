@@ -1,7 +1,7 @@
 """RMS norm with residual and its 8-bit outputs, against 64 bits and against the library's quantizers.
 
 Tolerance of an f32 y, u = 2^-24: s is one rounding (u); the sum of squares is
-a chain of c fma per thread (c = 16, or 4 * ceil(k / 4096) for rows longer
+a chain of c fma per thread (at most 16, or 8 * ceil(k / 8192) for rows longer
 than 16384), 6 steps over the wave and at most 16 over the workgroup, on
 squares that are 2u off: (c + 24) u, halved by the root; division by k, eps,
 root, reciprocal and two products add at most 6u.  In all (c / 2 + 19) u of
@@ -49,7 +49,7 @@ def inputs(m, k, t, seed, ld=None, offset=0):
 
 
 def bound(k, t):
-    chain = 16 if k <= 16384 else 4 * -(-k // 4096)
+    chain = max(16, 8 * -(-k // 8192))
     return (chain / 2 + 19) * 2.0 ** -24 + HALF_ULP[t]
 
 
