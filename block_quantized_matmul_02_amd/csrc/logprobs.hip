@@ -10,16 +10,19 @@
 //
 // Top alternatives: a logit and its column make one 64-bit key that orders
 // them (value first, then the lower column), so equal logits need no care.
-// A wave keeps its 64 best keys sorted, one per lane; the K-th of them is a
-// bound, and only logits above it are appended to a short buffer in LDS that
-// is sorted (bitonic, DPP exchanges) and merged when it holds a wave of them.
-// A wave's first step has no bound yet: it takes the K-th of the lanes' own
-// maxima, which at least K logits reach.  Random logits pass the bound about
-// K (1 + log(length / 1024)) times in all; rising ones every time, where
-// the lanes' maxima bound what a step of 1024 can append.
+// A wave keeps a bound that the K-th best is known to reach; logits above it
+// are appended to a short buffer in LDS, and once that holds a wave of them it
+// is sorted (bitonic, DPP exchanges) and merged into the 64 best, one per lane,
+// whose K-th raises the bound.  So does the K-th of the lanes' running maxima (a
+// sort of 64 floats), from the first step on and whenever a logit passes, and a
+// workgroup's waves share their bounds.  Random logits pass about
+// K (1 + log(length / 1024)) times in all; rising ones every time, where the
+// lanes' maxima limit what a step of 1024 can append.  What waits at the end is
+// sorted once for the whole workgroup.
 //
-// HBM-bound (one read); with few rows the columns are split over workgroups
-// and a second, one-wave launch joins their sums and lists.
+// HBM-bound (one read, the next two steps' loads in flight); with few rows the
+// columns are split over workgroups and a second, one-wave launch joins their
+// sums and lists.
 #include "values.h"
 
 namespace bqm {
@@ -29,8 +32,8 @@ constexpr int kLpWaves = kLpThreads / 64;
 constexpr int kLpVals = 16;                         // logits per thread and step
 constexpr int kLpStep = kLpThreads * kLpVals;       // logits per workgroup and step
 constexpr int kLpMaxSplits = 64;                    // a lane for each in the joining launch
-constexpr int kLpWantGroups = 2048;                 // workgroups that fill the card: 8 per compute unit
-constexpr int kLpMaxN = 1 << 30;                    // 32-bit columns
+constexpr int kLpWantGroups = 512;                  // workgroups that fill the card: 2 per compute unit
+constexpr int kLpMaxN = 1 << 28;                    // a row's bytes in 31 bits
 constexpr float kLowest = -3.402823466e+38f;
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -99,6 +102,23 @@ __device__ __forceinline__ u64 keep(u64 v) {
     return ((threadIdx.x & H) != 0) == (v < o) ? v : o;
 }
 
+template <int M>
+__device__ __forceinline__ float keepf(float v) {
+    constexpr int H = M >= 32 ? 32 : M >= 16 ? 16 : M >= 8 ? 8 : M >= 4 ? 4 : M >= 2 ? 2 : 1;
+    const float o = __builtin_bit_cast(float, lane_xor<M>(__builtin_bit_cast(unsigned, v)));
+    return (threadIdx.x & H) ? fminf(v, o) : fmaxf(v, o);
+}
+
+// 64 values (no NaN), one per lane, to descending order.
+__device__ __forceinline__ float sort64f(float v) {
+    v = keepf<1>(v);
+    v = keepf<1>(keepf<3>(v));
+    v = keepf<1>(keepf<2>(keepf<7>(v)));
+    v = keepf<1>(keepf<2>(keepf<4>(keepf<15>(v))));
+    v = keepf<1>(keepf<2>(keepf<4>(keepf<8>(keepf<31>(v)))));
+    return keepf<1>(keepf<2>(keepf<4>(keepf<8>(keepf<16>(keepf<63>(v))))));
+}
+
 // 64 keys, one per lane, to descending order.
 __device__ __forceinline__ u64 sort64(u64 v) {
     v = keep<1>(v);
@@ -121,14 +141,21 @@ __device__ __forceinline__ u64 from_lane(u64 v, int lane) {
            (unsigned)__builtin_amdgcn_readlane((int)v, lane);
 }
 
-// One wave's best keys so far: 64 sorted in registers, and up to 127 more in
-// LDS that are above the bound and wait to be merged.
+// Keys that can wait: fewer than a wave of them, and what a step appends before
+// they are looked at: up to 16 of each lane that reaches the bound, at most K
+// lanes or, where the bound is a value, K - 1 above it and 8 equal to it.
+constexpr int kLpTies = 8;
+constexpr int kLpWaiting = 64 + (BQM_LOGPROBS_MAX_TOP + kLpTies) * kLpVals;
+
+// One wave's best keys so far: 64 sorted in registers (none before the first
+// merge), and more in LDS that are above the bound and wait.
 struct WaveTop {
     u64 list;    // this lane's key of the sorted list
     u64 bound;   // a key must be above it; 0: no bound yet
-    u64 *buf;    // 128 keys
+    u64 *buf;    // kLpWaiting keys
     int waiting;
     int top;
+    bool merged;
 
     __device__ __forceinline__ void init(u64 *b, int k) {
         list = 0;
@@ -136,37 +163,41 @@ struct WaveTop {
         buf = b;
         waiting = 0;
         top = k;
+        merged = false;
     }
 
     __device__ __forceinline__ void raise(u64 b) { bound = b > bound ? b : bound; }
 
-    __device__ __forceinline__ void merge(int count) {
-        const int lane = threadIdx.x & 63;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        const u64 mine = lane < count ? buf[lane] : 0;
-        list = merge64(list, sort64(mine));
+    // Takes in one key per lane (0: none).
+    __device__ __forceinline__ void take(u64 mine) {
+        mine = sort64(mine);
+        list = merged ? merge64(list, mine) : mine;
+        merged = true;
         raise(from_lane(list, top - 1));
     }
 
-    __device__ __forceinline__ void append(bool take, u64 key) {
-        const u64 mask = __ballot(take);
+    __device__ __forceinline__ void append(bool pass, u64 key) {
+        const u64 mask = __ballot(pass);
         if (mask == 0) return;
         const int before = __builtin_amdgcn_mbcnt_hi((unsigned)(mask >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)mask, 0));
-        if (take) buf[waiting + before] = key;
+        if (pass) buf[waiting + before] = key;
         waiting += __popcll(mask);
-        if (waiting >= 64) {
-            merge(64);
-            const int lane = threadIdx.x & 63;
-            const int rest = waiting - 64;
-            const u64 moved = lane < rest ? buf[64 + lane] : 0;
+    }
+
+    // Merges whole waves of waiting keys.
+    __device__ __forceinline__ void drain() {
+        while (waiting >= 64) {
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            if (lane < rest) buf[lane] = moved;
-            waiting = rest;
+            waiting -= 64;
+            take(buf[waiting + (threadIdx.x & 63)]);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         }
     }
 
     __device__ __forceinline__ void finish() {
-        if (waiting) merge(waiting);
+        const int lane = threadIdx.x & 63;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (waiting) take(lane < waiting ? buf[lane] : 0);
         waiting = 0;
     }
 };
@@ -228,41 +259,62 @@ template <typename T, bool TOP>
 __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LpArgs a) {
     constexpr int V = 16 / sizeof(T);      // logits of a 16-byte load
     constexpr int U = kLpVals / V;
-    __shared__ u64 buf[kLpWaves][128];
+    __shared__ u64 buf[kLpWaves][kLpWaiting];
+    __shared__ u64 lists[kLpWaves][64];
     __shared__ Sums part[kLpWaves];
+    __shared__ u64 shared_bound;           // the highest of the waves' bounds
+    __shared__ int counts[kLpWaves];       // keys that wait (under 64), + 64 if the wave has a list
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t row = blockIdx.x / (unsigned)a.splits;
     const int split = blockIdx.x % (unsigned)a.splits;
     const T *l = static_cast<const T *>(a.logits) + row * a.ld;
-    // loads are aligned to 16 bytes: the row starts `skip` logits into the first
+    // loads are aligned to 16 bytes: the row starts `skip` logits into the
+    // first; past its last dword they give zeros
     const int skip = (int)((reinterpret_cast<uintptr_t>(l) & 15) / sizeof(T));
+    const __amdgpu_buffer_rsrc_t rl = mx_rsrc(l - skip, ((int64_t)(a.n + skip) * sizeof(T) + 3) & ~3ll);
     const int steps = (a.n + skip + kLpStep - 1) / kLpStep;
     const int each = (steps + a.splits - 1) / a.splits;
     const int last = min(steps, (split + 1) * each);
 
+    struct Raw {
+        u32x4 q[U];
+    };
+    auto load = [&](Raw &w, int st) {
+        const uint32_t off = (uint32_t)(st * kLpStep + wave * (64 * kLpVals) + lane * V) * (uint32_t)sizeof(T);
+#pragma unroll
+        for (int u = 0; u < U; u++) w.q[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rl, off + u * 1024, 0, 0));
+    };
+
     Sums r = {kLowest, 0.0f, 0.0f};
     WaveTop best;
     best.init(buf[wave], a.top);
-    for (int st = split * each; st < last; st++) {
+    float most = -__builtin_inff();   // this lane's largest logit so far
+    int passed = 0;                   // lanes that passed since the bound was last looked for
+    auto step = [&](const Raw &w, int st) {
+        u64 others = 0;
+        if constexpr (TOP) others = *const_cast<volatile u64 *>(&shared_bound);
         const int i0 = st * kLpStep + wave * (64 * kLpVals) + lane * V - skip;
+        auto column = [&](int e) { return i0 + (e / V) * 64 * V + e % V; };
         float v[kLpVals];
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            const int i = i0 + u * 64 * V;
-            if (i >= 0 && i + V <= a.n) {
-                typedef T vec __attribute__((ext_vector_type(V)));
-                const vec q = *reinterpret_cast<const vec *>(l + i);
+            typedef T vec __attribute__((ext_vector_type(V)));
+            const vec q = __builtin_bit_cast(vec, w.q[u]);
 #pragma unroll
-                for (int e = 0; e < V; e++) v[u * V + e] = (float)q[e];
-            } else {
-#pragma unroll
-                for (int e = 0; e < V; e++) v[u * V + e] = i + e >= 0 && i + e < a.n ? (float)l[i + e] : -__builtin_inff();
-            }
+            for (int e = 0; e < V; e++) v[u * V + e] = (float)q[e];
         }
-        float big = v[0];
+        // columns outside the row: only in its first and last step
+        if (st == 0 || (st + 1) * kLpStep > a.n + skip) {
 #pragma unroll
-        for (int e = 1; e < kLpVals; e++) big = fmaxf(big, v[e]);   // drops NaN
+            for (int e = 0; e < kLpVals; e++) v[e] = column(e) >= 0 && column(e) < a.n ? v[e] : -__builtin_inff();
+        }
+        float four[kLpVals / 4];   // fmaxf drops NaN
+#pragma unroll
+        for (int g = 0; g < kLpVals / 4; g++) four[g] = fmaxf(fmaxf(v[4 * g], v[4 * g + 1]), fmaxf(v[4 * g + 2], v[4 * g + 3]));
+        float big = four[0];
+#pragma unroll
+        for (int g = 1; g < kLpVals / 4; g++) big = fmaxf(big, four[g]);
 
         const float m = fmaxf(r.m, big);
         const float dm = fmaxf(r.m - m, -200.0f);
@@ -279,66 +331,117 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LpArgs a) {
         }
 
         if constexpr (TOP) {
-            auto column = [&](int e) { return i0 + (e / V) * 64 * V + e % V; };
-            if ((best.bound >> 32) == 0) {
-                // no bound, or one whose value is NaN: compare whole keys
+            auto key = [&](int e) {
+                const int c = column(e);
+                return c >= 0 && c < a.n ? key_of(v[e], c) : 0;
+            };
+            // the K-th of the lanes' best keys: at least K keys reach it
+            auto raise_by_keys = [&]() {
                 u64 mine = 0;
 #pragma unroll
                 for (int e = 0; e < kLpVals; e++) {
-                    const int c = column(e);
-                    const u64 key = c >= 0 && c < a.n ? key_of(v[e], c) : 0;
-                    mine = key > mine ? key : mine;
+                    const u64 k = key(e);
+                    mine = k > mine ? k : mine;
                 }
                 if (__popcll(__ballot(mine > best.bound)) >= a.top) best.raise(from_lane(sort64(mine), a.top - 1) - 1);
+            };
+            best.raise(others);
+            const u64 before = best.bound;
+            const bool open = (before >> 32) == 0;   // no bound, or one whose value is NaN
+            // columns past the bound's own lose ties against it
+            const float low0 = value_of((unsigned)(before >> 32));
+            const bool strict = st * kLpStep + wave * (64 * kLpVals) - skip > (int)~(unsigned)before;
+            const u64 above = __ballot(big >= kLowest && (open || big > low0 || (!strict && big == low0)));
+            most = fmaxf(most, big);
+            if (!open && above == 0) return;
+            // The K-th of the lanes' running maxima is a bound, which all of its
+            // value pass; keys decide where many lanes are equal to it.  Looked
+            // for when K lanes pass at once and after every 8 + K / 2 that pass:
+            // the sort costs as much as appending a few keys.
+            const int lanes = __popcll(above);
+            passed += lanes;
+            if (open || lanes >= a.top || passed >= 8 + a.top / 2) {
+                passed = 0;
+                const float kth = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sort64f(most)), a.top - 1));
+                if (kth >= kLowest && __popcll(__ballot(most == kth)) <= kLpTies)
+                    best.raise(((u64)order_of(kth) << 32) - 1);
+                else if (open || lanes >= a.top)
+                    raise_by_keys();
+            }
+            if ((best.bound >> 32) != 0) {
+                const float low = value_of((unsigned)(best.bound >> 32));
+#pragma unroll
+                for (int g = 0; g < kLpVals / 4; g++) {
+                    if (__ballot(four[g] >= low) == 0) continue;
+#pragma unroll
+                    for (int e = 4 * g; e < 4 * g + 4; e++) {
+                        if (__ballot(v[e] >= low) == 0) continue;
+                        const u64 k = key(e);
+                        best.append(k > best.bound, k);
+                    }
+                }
+                best.drain();
+            } else {
 #pragma unroll 1
                 for (int e = 0; e < kLpVals; e++) {
                     float ve = v[0];
 #pragma unroll
                     for (int q = 1; q < kLpVals; q++) ve = e == q ? v[q] : ve;
                     const int c = column(e);
-                    const u64 key = c >= 0 && c < a.n ? key_of(ve, c) : 0;
-                    best.append(key > best.bound, key);
-                }
-            } else {
-                // later columns lose ties, so only a larger value passes
-                float low = value_of((unsigned)(best.bound >> 32));
-                const u64 above = __ballot(big > low);
-                if (above != 0) {
-                    if (__popcll(above) >= a.top) {
-                        // rising logits: K lanes' maxima pass, so the K-th of them is a bound
-                        u64 mine = 0;
-#pragma unroll
-                        for (int e = 0; e < kLpVals; e++) {
-                            const int c = column(e);
-                            const u64 key = c >= 0 && c < a.n ? key_of(v[e], c) : 0;
-                            mine = key > mine ? key : mine;
-                        }
-                        best.raise(from_lane(sort64(mine), a.top - 1) - 1);
-                        low = value_of((unsigned)(best.bound >> 32));
-                    }
-#pragma unroll
-                    for (int e = 0; e < kLpVals; e++) {
-                        if (__ballot(v[e] >= low) == 0) continue;
-                        const int c = column(e);
-                        const u64 key = c >= 0 && c < a.n ? key_of(v[e], c) : 0;
-                        best.append(key > best.bound, key);
-                    }
+                    const u64 k = c >= 0 && c < a.n ? key_of(ve, c) : 0;
+                    best.append(k > best.bound, k);
+                    best.drain();
                 }
             }
+            if (best.bound > before && lane == 0) atomicMax(&shared_bound, best.bound);
         }
+    };
+
+    Raw w0, w1;
+    load(w0, split * each);
+    load(w1, split * each + 1);
+    if constexpr (TOP) {
+        if (threadIdx.x == 0) shared_bound = 0;
+        __syncthreads();
+    }
+#pragma unroll 1
+    for (int st = split * each; st < last; st += 2) {
+        step(w0, st);
+        load(w0, st + 2);
+        if (st + 1 < last) step(w1, st + 1);
+        load(w1, st + 3);
     }
 
     r = join_wave(r);
     if constexpr (TOP) {
-        best.finish();
-        buf[wave][lane] = best.list;
+        lists[wave][lane] = best.list;
+        if (lane == 0) counts[wave] = best.waiting + (best.merged ? 64 : 0);
     }
     if (lane == 0) part[wave] = r;
     __syncthreads();
     if (wave != 0) return;
-    for (int w = 1; w < kLpWaves; w++) {
-        r = join(r, part[w]);
-        if constexpr (TOP) best.list = merge64(best.list, buf[w][lane]);
+    for (int w = 1; w < kLpWaves; w++) r = join(r, part[w]);
+    if constexpr (TOP) {
+        // the waves' lists are sorted; what waits is taken a wave of keys at a time
+        int first[kLpWaves + 1];
+        first[0] = 0;
+#pragma unroll
+        for (int w = 0; w < kLpWaves; w++) {
+            const int c = __builtin_amdgcn_readfirstlane(counts[w]);
+            first[w + 1] = first[w] + (c & 63);
+            if (w > 0 && c >= 64) {
+                best.list = best.merged ? merge64(best.list, lists[w][lane]) : lists[w][lane];
+                best.merged = true;
+            }
+        }
+        for (int j0 = 0; j0 < first[kLpWaves]; j0 += 64) {
+            const int j = j0 + lane;
+            u64 k = 0;
+#pragma unroll
+            for (int w = 0; w < kLpWaves; w++)
+                if (j >= first[w] && j < first[w + 1]) k = buf[w][j - first[w]];
+            best.take(k);
+        }
     }
     if (a.splits == 1) {
         write_row<T>(a, row, r, best.list);
@@ -352,7 +455,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LpArgs a) {
 // Joins a row's splits: one wave.
 template <typename T>
 __global__ __launch_bounds__(64) void logprobs_join_kernel(LpArgs a) {
-    __shared__ u64 buf[128];
+    __shared__ u64 buf[128];   // fewer than 64 waiting and a wave's worth at a time
     const int lane = threadIdx.x;
     const int64_t row = blockIdx.x;
     Sums r = {kLowest, 0.0f, 0.0f};
@@ -383,6 +486,7 @@ __global__ __launch_bounds__(64) void logprobs_join_kernel(LpArgs a) {
 #pragma unroll
                 for (int q = 1; q < 8; q++) key = u == q ? k[q] : key;
                 best.append(key > best.bound, key);
+                best.drain();
             }
         }
         best.finish();

@@ -13,12 +13,6 @@ struct MgArgs {
     int mtiles, ntiles;
 };
 
-// A buffer whose reads past `bytes` give zeros.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t mx_rsrc(const void *base, int64_t bytes) {
-    const uint32_t b = bytes <= 0 ? 0u : bytes > 0x7FFFFFF0ll ? 0x7FFFFFF0u : (uint32_t)bytes;
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)b, 0x00020000);
-}
-
 // Widest aligned loads of scale rows of `nblk` bytes: 16, 4 or 1.
 inline int scale_load(int nblk, const void *a, const void *b) {
     if (nblk % 16 == 0 && aligned(a, 16) && aligned(b, 16)) return 16;

@@ -23,6 +23,12 @@ template <> struct Vec<__bf16> {
     typedef __bf16 x8 __attribute__((ext_vector_type(8)));
 };
 
+// A buffer whose reads past `bytes` give zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t mx_rsrc(const void *base, int64_t bytes) {
+    const uint32_t b = bytes <= 0 ? 0u : bytes > 0x7FFFFFF0ll ? 0x7FFFFFF0u : (uint32_t)bytes;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)b, 0x00020000);
+}
+
 inline int type_bytes(int type) { return type == BQM_F32 ? 4 : 2; }
 inline bool type_known(int type) { return type == BQM_F32 || type == BQM_F16 || type == BQM_BF16; }
 
