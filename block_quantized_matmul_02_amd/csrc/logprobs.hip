@@ -176,12 +176,35 @@ struct WaveTop {
         raise(from_lane(list, top - 1));
     }
 
+    // Appends a key of each lane that has one to append.
     __device__ __forceinline__ void append(bool pass, u64 key) {
         const u64 mask = __ballot(pass);
         if (mask == 0) return;
         const int before = __builtin_amdgcn_mbcnt_hi((unsigned)(mask >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)mask, 0));
         if (pass) buf[waiting + before] = key;
         waiting += __popcll(mask);
+    }
+
+    // Appends those of a lane's N keys that are above the bound: the lanes'
+    // counts are summed up across the wave, and each lane writes its own behind
+    // the lanes before it, without a branch.
+    template <int N>
+    __device__ __forceinline__ void append(const u64 (&k)[N]) {
+        int n = 0;
+#pragma unroll
+        for (int e = 0; e < N; e++) n += k[e] > bound ? 1 : 0;
+        int sum = n;   // over lanes 0 .. this one
+        sum += __builtin_amdgcn_update_dpp(0, sum, 0x111, 0xF, 0xF, false);   // 1, 2, 4, 8 lanes of a row of 16 back
+        sum += __builtin_amdgcn_update_dpp(0, sum, 0x112, 0xF, 0xF, false);
+        sum += __builtin_amdgcn_update_dpp(0, sum, 0x114, 0xF, 0xF, false);
+        sum += __builtin_amdgcn_update_dpp(0, sum, 0x118, 0xF, 0xF, false);
+        sum += __builtin_amdgcn_update_dpp(0, sum, 0x142, 0xA, 0xF, false);   // row 0 to 1, row 2 to 3
+        sum += __builtin_amdgcn_update_dpp(0, sum, 0x143, 0xC, 0xF, false);   // rows 0, 1 to 2, 3
+        u64 *to = buf + waiting + sum - n;
+#pragma unroll
+        for (int e = 0; e < N; e++)
+            if (k[e] > bound) *to++ = k[e];
+        waiting += __builtin_amdgcn_readlane(sum, 63);
     }
 
     // Merges whole waves of waiting keys.
@@ -368,7 +391,15 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LpArgs a) {
                 else if (open || lanes >= a.top)
                     raise_by_keys();
             }
-            if ((best.bound >> 32) != 0) {
+            // Append what passes: in one go where many lanes have something, else
+            // by looking for the few.  (Without a bound on the values fewer than K
+            // lanes have keys at all.)
+            if ((best.bound >> 32) == 0 || lanes > 8) {
+                u64 k[kLpVals];
+#pragma unroll
+                for (int e = 0; e < kLpVals; e++) k[e] = key(e);
+                best.append(k);
+            } else {
                 const float low = value_of((unsigned)(best.bound >> 32));
 #pragma unroll
                 for (int g = 0; g < kLpVals / 4; g++) {
@@ -380,19 +411,8 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LpArgs a) {
                         best.append(k > best.bound, k);
                     }
                 }
-                best.drain();
-            } else {
-#pragma unroll 1
-                for (int e = 0; e < kLpVals; e++) {
-                    float ve = v[0];
-#pragma unroll
-                    for (int q = 1; q < kLpVals; q++) ve = e == q ? v[q] : ve;
-                    const int c = column(e);
-                    const u64 k = c >= 0 && c < a.n ? key_of(ve, c) : 0;
-                    best.append(k > best.bound, k);
-                    best.drain();
-                }
             }
+            best.drain();
             if (best.bound > before && lane == 0) atomicMax(&shared_bound, best.bound);
         }
     };
@@ -455,7 +475,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LpArgs a) {
 // Joins a row's splits: one wave.
 template <typename T>
 __global__ __launch_bounds__(64) void logprobs_join_kernel(LpArgs a) {
-    __shared__ u64 buf[128];   // fewer than 64 waiting and a wave's worth at a time
+    __shared__ u64 buf[64 + 512];   // fewer than 64 waiting and eight waves' worth
     const int lane = threadIdx.x;
     const int64_t row = blockIdx.x;
     Sums r = {kLowest, 0.0f, 0.0f};
@@ -480,14 +500,8 @@ __global__ __launch_bounds__(64) void logprobs_join_kernel(LpArgs a) {
             u64 k[8];
 #pragma unroll
             for (int u = 0; u < 8; u++) k[u] = i0 + 64 * u + lane < all ? keys[i0 + 64 * u + lane] : 0;
-#pragma unroll 1
-            for (int u = 0; u < 8; u++) {
-                u64 key = k[0];
-#pragma unroll
-                for (int q = 1; q < 8; q++) key = u == q ? k[q] : key;
-                best.append(key > best.bound, key);
-                best.drain();
-            }
+            best.append(k);
+            best.drain();
         }
         best.finish();
     }

@@ -127,7 +127,10 @@ int bqm_mxfp4_gemm(const uint8_t *w, const uint8_t *ws, const uint8_t *xq, const
  * activations, 1 <= m <= BQM_MXFP4_GEMV_MAX_M:
  * y[t][r] = sum_b 2^(ws[r][b] - 127) * sum_{i in b} x[t][i] * e2m1(w[r][i]),
  * f32 accumulation.  A token's result does not depend on m or on the other
- * tokens.
+ * tokens.  An infinity or NaN among a token's activations makes that token's
+ * results infinite or NaN.  Scales are at most 252, which is what
+ * bqm_mxfp4_quantize writes for finite values, or 255 (NaN): with 253 and 254
+ * the largest codes leave the range of f32.  Bits of x below 2^-133 are lost.
  *   x : f32 [m][k], 16-byte aligned, dense; the rest as bqm_mxfp4_gemm.
  */
 int bqm_mxfp4_gemv(const uint8_t *w, const uint8_t *ws, const float *x, float *y, int m, int k, int n, void *stream);
