@@ -109,7 +109,7 @@ struct TokenSum {
 
 // WIDE: scale rows are whole, aligned dwords (k % 128 == 0); else bytes.
 template <int G, bool WIDE>
-__global__ __launch_bounds__(kMvMaxWaves * 64, G == 1 ? (WIDE ? 4 : 3) : 2) void mxfp4_gemv_kernel(MvArgs a) {
+__global__ __launch_bounds__(kMvMaxWaves * 64, 2) void mxfp4_gemv_kernel(MvArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -155,7 +155,7 @@ __global__ __launch_bounds__(kMvMaxWaves * 64, G == 1 ? (WIDE ? 4 : 3) : 2) void
 
         // x operands: a token's 512 values are eight per lane, its three parts
         // three rows; a lane then takes row r16 of each group's operand.  The
-        // first group's values are asked for before the first weights.
+        // values are asked for before the first weights, all at once.
         MvTile t0, t1;
         v8bf xop[G][16];
         {
@@ -163,22 +163,23 @@ __global__ __launch_bounds__(kMvMaxWaves * 64, G == 1 ? (WIDE ? 4 : 3) : 2) void
             const __amdgpu_buffer_rsrc_t rx = mx_rsrc(a.x, 4ll * a.m * a.k);
             // k % 32 == 0: a lane's eight values are in or out of the row together
             const uint32_t off = 32 * blk0 + 8 * lane < a.k ? (uint32_t)(4 * (32 * blk0 + 8 * lane)) : 0x80000000u;
+            // a group's five tokens and, of three groups, the sixteenth
+            constexpr int kTok = G == 3 ? 6 : 5;
+            u32x4 all[G][kTok][2];
 #pragma unroll
-            for (int grp = 0; grp < G; grp++) {
-                // the group's five tokens and, of three groups, the sixteenth
-                constexpr int kTok = G == 3 ? 6 : 5;
-                u32x4 raw[kTok][2];
+            for (int grp = 0; grp < G; grp++)
 #pragma unroll
                 for (int i = 0; i < kTok; i++) {
                     // tokens past the last read zeros
                     const uint32_t at = off + (uint32_t)(4 * a.k) * (i < 5 ? 5 * grp + i : 15);
-                    raw[i][0] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, at, 0, 0));
-                    raw[i][1] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, at + 16, 0, 0));
+                    all[grp][i][0] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, at, 0, 0));
+                    all[grp][i][1] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, at + 16, 0, 0));
                 }
-                if (grp == 0) {
-                    load(t0, 0);
-                    if constexpr (G < 3) load(t1, 1);
-                }
+            load(t0, 0);
+            if constexpr (G < 3) load(t1, 1);
+#pragma unroll
+            for (int grp = 0; grp < G; grp++) {
+                const auto &raw = all[grp];
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
                 for (int i = 0; i < kTok; i++) {

@@ -1,16 +1,17 @@
 // The MXFP4 x MXFP4 product for few tokens (up to 64, as long as their codes
-// fit in LDS): HBM-bound, every weight read once.
+// fit in registers or LDS): HBM-bound, every weight read once.
 //
-//  * The workgroup keeps the tokens' codes and scales in LDS, in the order in
-//    which the matrix cores take them: a lane's 16 bytes of each 16-token
-//    group and 128-k step follow the lane before's, and its four scales of 512
-//    k are one dword.
+//  * Up to k = 4096 a wave has one 512-k slice of every tile and keeps the
+//    tokens' operand for it in registers.  Beyond, the workgroup keeps the
+//    tokens' codes and scales in LDS, in the order in which the matrix cores
+//    take them: a lane's 16 bytes of each 16-token group and 128-k step follow
+//    the lane before's, and its four scales of 512 k are one dword.
 //  * A wave streams tiles of 16 weight rows, 512 k at a time, straight from
 //    memory into the operand registers of v_mfma_scale_f32_16x16x128 (lane:
 //    row r = l % 16, block 4 i + l / 16 of step i), kAhead items ahead.
-//  * The workgroup's waves share a tile's k (`parts` of them) or take tiles
-//    of their own, as many along k as leave every wave work; parts meet in
-//    LDS, added in wave order.
+//  * The workgroup's waves share a tile's k (`parts` of them), or where a row
+//    has fewer than eight slices several tiles; parts meet in LDS, added in
+//    wave order.
 #include <type_traits>
 
 #include "mxfp4.h"
@@ -40,8 +41,9 @@ __device__ __forceinline__ v4f ms_mfma(u32x4 a, u32x4 b, v4f c, int sa, int sb) 
 }
 
 // G: groups of 16 tokens; SW: scale rows in aligned 16-byte pieces (16) or bytes (1).
-template <int G, int SW>
-__global__ __launch_bounds__(kMsWaves * 64, G == 1 ? 4 : 2) void mxfp4_stream_kernel(MsArgs d) {
+// XREG: a wave has one slice (k <= 4096), whose operand stays in its registers.
+template <int G, int SW, bool XREG>
+__global__ __launch_bounds__(kMsWaves * 64, G == 1 && !XREG ? 4 : 2) void mxfp4_stream_kernel(MsArgs d) {
     constexpr int kAhead = 3;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const MgArgs &a = d.a;
@@ -56,7 +58,7 @@ __global__ __launch_bounds__(kMsWaves * 64, G == 1 ? 4 : 2) void mxfp4_stream_ke
 
     uint8_t *const xc = lds;                                              // [G][slices][4 steps][64 lanes][16]
     int *const xsc = reinterpret_cast<int *>(lds + G * d.slices * 4096);  // [G][slices][64 lanes]
-    v4f *const red = reinterpret_cast<v4f *>(lds + G * d.slices * (4096 + 256));   // [waves][64 lanes]
+    v4f *const red = reinterpret_cast<v4f *>(lds + (XREG ? 0 : G * d.slices * (4096 + 256)));   // [waves][64 lanes]
 
     struct Tile {
         u32x4 c[4];
@@ -92,36 +94,61 @@ __global__ __launch_bounds__(kMsWaves * 64, G == 1 ? 4 : 2) void mxfp4_stream_ke
             next_tile += hop;
         }
     };
-    // this lane's four scales, one a byte
-    auto scales = [&](const Tile &t) {
+    // this lane's four scales, one a byte, from what SW loads
+    auto scales = [&](const unsigned (&s)[4]) {
         if constexpr (SW == 16) {
             // byte g4 of each dword
             const unsigned sel = 0x0C0C0400u + 0x0101u * (unsigned)g4;
-            const unsigned lo = __builtin_amdgcn_perm(t.s[1], t.s[0], sel), hi = __builtin_amdgcn_perm(t.s[3], t.s[2], sel);
+            const unsigned lo = __builtin_amdgcn_perm(s[1], s[0], sel), hi = __builtin_amdgcn_perm(s[3], s[2], sel);
             return (int)(lo | hi << 16);
         } else {
-            return (int)(t.s[0] | t.s[1] << 8 | t.s[2] << 16 | t.s[3] << 24);
+            return (int)(s[0] | s[1] << 8 | s[2] << 16 | s[3] << 24);
         }
     };
 
+    // The tokens' codes and scales; tokens and blocks past the ends are zeros.
+    const __amdgpu_buffer_rsrc_t rx = mx_rsrc(a.xq, a.m * rb), rxs = mx_rsrc(a.xs, (int64_t)a.m * nblk);
+    auto x_codes = [&](int grp, int b, bool in) {
+        return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                   rx, in && b < nblk ? (uint32_t)((16 * grp + r16) * rb + 16 * b) : 0x80000000u, 0, 0));
+    };
+    auto x_scales = [&](unsigned (&s)[4], int grp, int slice, bool in) {
+        if constexpr (SW == 16) {
+            const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                rxs, in && 16 * slice < nblk ? (uint32_t)((16 * grp + r16) * nblk + 16 * slice) : 0x80000000u, 0, 0));
+#pragma unroll
+            for (int i = 0; i < 4; i++) s[i] = v[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int b = 16 * slice + 4 * i + g4;
+                s[i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rxs, in && b < nblk ? (uint32_t)((16 * grp + r16) * nblk + b) : 0x80000000u, 0, 0);
+            }
+        }
+    };
+    u32x4 xr[XREG ? G : 1][4];
+    unsigned xrs[XREG ? G : 1][4];
     Tile it[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; i++) load(it[i]);
-
-    // The tokens' codes and scales, several loads of a thread at a time; tokens
-    // and blocks past the ends are read as zeros.
-    {
+    if constexpr (XREG) {
+#pragma unroll
+        for (int grp = 0; grp < G; grp++) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) xr[grp][i] = x_codes(grp, 16 * wpart + 4 * i + g4, sub < d.subs);
+            x_scales(xrs[grp], grp, wpart, sub < d.subs);
+        }
+    }
+    if constexpr (!XREG) {
+        // several loads of a thread at a time
         constexpr int U = 8;
-        const __amdgpu_buffer_rsrc_t rx = mx_rsrc(a.xq, a.m * rb), rxs = mx_rsrc(a.xs, (int64_t)a.m * nblk);
         const int steps = G * d.slices * 4, per = d.slices * 4;   // a wave writes a step's 1 KiB
         for (int st0 = wave; st0 < steps; st0 += U * kMsWaves) {
             u32x4 v[U];
 #pragma unroll
             for (int u = 0; u < U; u++) {
-                const int st = st0 + u * kMsWaves, grp = st / per, b = (st - grp * per) * 4 + g4;
-                const bool in = st < steps && b < nblk;
-                v[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                           rx, in ? (uint32_t)((16 * grp + r16) * rb + 16 * b) : 0x80000000u, 0, 0));
+                const int st = st0 + u * kMsWaves, grp = st / per;
+                v[u] = x_codes(grp, (st - grp * per) * 4 + g4, st < steps);
             }
 #pragma unroll
             for (int u = 0; u < U; u++)
@@ -133,20 +160,14 @@ __global__ __launch_bounds__(kMsWaves * 64, G == 1 ? 4 : 2) void mxfp4_stream_ke
 #pragma unroll
             for (int u = 0; u < V; u++) {
                 const int sl = sl0 + u * kMsWaves, grp = sl / d.slices;
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int b = 16 * (sl - grp * d.slices) + 4 * e + g4;
-                    const bool in = sl < G * d.slices && b < nblk;
-                    v[u][e] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rxs, in ? (uint32_t)((16 * grp + r16) * nblk + b) : 0x80000000u, 0, 0);
-                }
+                x_scales(v[u], grp, sl - grp * d.slices, sl < G * d.slices);
             }
 #pragma unroll
             for (int u = 0; u < V; u++)
-                if (sl0 + u * kMsWaves < G * d.slices)
-                    xsc[(sl0 + u * kMsWaves) * 64 + lane] = (int)(v[u][0] | v[u][1] << 8 | v[u][2] << 16 | v[u][3] << 24);
+                if (sl0 + u * kMsWaves < G * d.slices) xsc[(sl0 + u * kMsWaves) * 64 + lane] = scales(v[u]);
         }
+        __syncthreads();
     }
-    __syncthreads();
 
     v4f acc[G] = {};
     int s = 0, first = blockIdx.x * d.subs;   // slice turn, the workgroup's current first tile
@@ -161,14 +182,22 @@ __global__ __launch_bounds__(kMsWaves * 64, G == 1 ? 4 : 2) void mxfp4_stream_ke
             for (int e = 0; e < 4; e++) acc[grp][e] = keep != 0.0f ? acc[grp][e] : 0.0f;
         const int slice = wpart + d.parts * s;
         const int at = slice < d.slices ? slice : 0;   // past the end: zero weights
-        const int sb = scales(q);
+        const int sb = scales(q.s);
 #pragma unroll
         for (int grp = 0; grp < G; grp++) {
-            const int sa = xsc[(grp * d.slices + at) * 64 + lane];
+            int sa;
+            if constexpr (XREG)
+                sa = scales(xrs[grp]);
+            else
+                sa = xsc[(grp * d.slices + at) * 64 + lane];
             const uint8_t *const p = xc + (grp * d.slices + at) * 4096 + 16 * lane;
             auto step = [&](auto qq) {
                 constexpr int Q = decltype(qq)::value;
-                const u32x4 x = *reinterpret_cast<const u32x4 *>(p + Q * 1024);
+                u32x4 x;
+                if constexpr (XREG)
+                    x = xr[grp][Q];
+                else
+                    x = *reinterpret_cast<const u32x4 *>(p + Q * 1024);
                 acc[grp] = ms_mfma<Q>(x, q.c[Q], acc[grp], sa, sb);
             };
             step(std::integral_constant<int, 0>{});
@@ -216,23 +245,21 @@ __global__ __launch_bounds__(kMsWaves * 64, G == 1 ? 4 : 2) void mxfp4_stream_ke
     }
 }
 
-template <int G, int SW>
+template <int G, int SW, bool XREG>
 static int launch_ms(MsArgs d, int cus, hipStream_t s) {
     static LaunchCache cache;
-    const void *fn = reinterpret_cast<const void *>(&mxfp4_stream_kernel<G, SW>);
+    const void *fn = reinterpret_cast<const void *>(&mxfp4_stream_kernel<G, SW, XREG>);
     const int rc = raise_lds_limit(cache, fn, kMsLds);
     if (rc) return rc;
     const int tiles = (d.a.n + 15) / 16;
     d.slices = (d.a.k + 511) / 512;
-    // waves along k: all of them, unless there are tiles enough for every wave
     d.parts = d.slices < kMsWaves ? d.slices : kMsWaves;
-    while (d.parts > 1 && tiles >= 2 * cus * (2 * kMsWaves / d.parts)) d.parts = (d.parts + 1) / 2;
     d.subs = kMsWaves / d.parts;
     d.per_wave = (d.slices + d.parts - 1) / d.parts;
-    const int bytes = (int)ms_lds(G, d.slices);
+    const int bytes = (int)ms_lds(XREG ? 0 : G, d.slices);
     const int units = (tiles + d.subs - 1) / d.subs;
     const int most = cus * blocks_per_cu(cache, fn, kMsWaves * 64, bytes, 2);
-    hipLaunchKernelGGL((mxfp4_stream_kernel<G, SW>), dim3(units < most ? units : most), dim3(kMsWaves * 64), bytes, s, d);
+    hipLaunchKernelGGL((mxfp4_stream_kernel<G, SW, XREG>), dim3(units < most ? units : most), dim3(kMsWaves * 64), bytes, s, d);
     return launch_status();
 }
 
@@ -240,17 +267,20 @@ template <int G>
 static int launch_ms_g(const MgArgs &a, hipStream_t s) {
     const MsArgs d = {a, 0, 0, 0, 0};
     const int cus = device_cus();
-    const bool wide = scale_load(a.k / 32, a.ws, a.ws) == 16;
-    return wide ? launch_ms<G, 16>(d, cus, s) : launch_ms<G, 1>(d, cus, s);
+    const bool wide = scale_load(a.k / 32, a.ws, a.xs) == 16;
+    if (a.k <= kMsWaves * 512) return wide ? launch_ms<G, 16, true>(d, cus, s) : launch_ms<G, 1, true>(d, cus, s);
+    return wide ? launch_ms<G, 16, false>(d, cus, s) : launch_ms<G, 1, false>(d, cus, s);
 }
 
-// Few tokens whose operand fits in LDS, against few enough rows that the large
-// kernel's 128-row tiles would leave half of the compute units idle (there
-// it takes 16.8 us where this takes 11.5: 16 x 4096 x 5152; with more rows it
-// is ahead, 19.7 to 29 at 64 x 4096 x 20480).
+// Few tokens whose operand fits, against few enough weight rows: with many the
+// other kernel's 128-row tiles fill the card and move the tokens' codes less
+// often.  Measured (this, tiles; us): 16 x 4096 x 64448 29.1, 29.7; 32 x 4096 x
+// 32768 19.8, 20.0, x 64448 33.6, 31.3; 48 x 4096 x 20480 18.2, 18.9; 64 x 4096
+// x 16384 19.1, 19.0, x 20480 21.2, 19.4; and 16 x 4096 x 5152 8.0, 16.8.
 bool mxfp4_stream_applies(int m, int k, int n) {
     const int groups = (m + 15) / 16;
-    return groups <= kMsMaxGroups && n <= 64 * device_cus() && ms_lds(groups, (int)(((int64_t)k + 511) / 512)) <= kMsLds;
+    if (groups > kMsMaxGroups || (groups > 1 && n > (groups > 3 ? 64 : 128) * device_cus())) return false;
+    return k <= kMsWaves * 512 || ms_lds(groups, (int)(((int64_t)k + 511) / 512)) <= kMsLds;
 }
 
 int mxfp4_stream(const MgArgs &a, hipStream_t s) {
