@@ -274,12 +274,15 @@ static int launch_ms_g(const MgArgs &a, hipStream_t s) {
 
 // Few tokens whose operand fits, against few enough weight rows: with many the
 // other kernel's 128-row tiles fill the card and move the tokens' codes less
-// often.  Measured (this, tiles; us): 16 x 4096 x 64448 29.1, 29.7; 32 x 4096 x
-// 32768 19.8, 20.0, x 64448 33.6, 31.3; 48 x 4096 x 20480 18.2, 18.9; 64 x 4096
-// x 16384 19.1, 19.0, x 20480 21.2, 19.4; and 16 x 4096 x 5152 8.0, 16.8.
+// often, the earlier the more groups of 16 tokens there are.  Measured (this,
+// tiles; us): 16 x 4096 x 5152 8.0, 16.8, x 64448 30.2, 31.5; 32 x 4096 x 32768
+// 20.3, 21.8; 48 x 4096 x 20480 18.6, 18.9, x 32768 23.9, 23.1; 64 x 4096 x
+// 8192 14.2, 18.5, x 12288 17.6, 18.9, x 16384 19.9, 19.0.
 bool mxfp4_stream_applies(int m, int k, int n) {
     const int groups = (m + 15) / 16;
-    if (groups > kMsMaxGroups || (groups > 1 && n > (groups > 3 ? 64 : 128) * device_cus())) return false;
+    if (groups > kMsMaxGroups) return false;
+    const int rows = groups == 2 ? 128 : groups == 3 ? 80 : 48;   // of weights for a compute unit, at most
+    if (groups > 1 && n > rows * device_cus()) return false;
     return k <= kMsWaves * 512 || ms_lds(groups, (int)(((int64_t)k + 511) / 512)) <= kMsLds;
 }
 
