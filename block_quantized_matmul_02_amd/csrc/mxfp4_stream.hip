@@ -12,6 +12,9 @@
 //  * The workgroup's waves share a tile's k (`parts` of them), or where a row
 //    has fewer than eight slices several tiles; parts meet in LDS, added in
 //    wave order.
+//
+// Weights from HBM: 16 x 4096 x 5152 8.0 us (latency: two tiles a workgroup),
+// 16 x 4096 x 64448 30.2 us (4.8 TB/s), 16 x 17408 x 20480 44 us (4.3 TB/s).
 #include <type_traits>
 
 #include "mxfp4.h"
@@ -239,9 +242,7 @@ __global__ __launch_bounds__(kMsWaves * 64, G == 1 && !XREG ? 4 : 2) void mxfp4_
     for (int j = 0; j < mine; j += kAhead) {
         item(it[0]);
         if (j + 1 < mine) item(it[1]);
-        if constexpr (kAhead == 3) {
-            if (j + 2 < mine) item(it[2]);
-        }
+        if (j + 2 < mine) item(it[2]);
     }
 }
 
