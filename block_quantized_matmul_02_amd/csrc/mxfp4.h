@@ -19,9 +19,10 @@ inline int scale_load(int nblk, const void *a, const void *b) {
     return nblk % 4 == 0 && aligned(a, 4) && aligned(b, 4) ? 4 : 1;
 }
 
-// The product for few tokens (mxfp4_stream.hip): whether it takes a shape, and
+// The product for few tokens (mxfp4_stream.hip): the groups of 16 tokens at a
+// time with which it takes a shape, 0 if the tiles (tile_cost us) should, and
 // its launch (arguments already checked by the GEMM entry).
-bool mxfp4_stream_applies(int m, int k, int n);
-int mxfp4_stream(const MgArgs &a, hipStream_t s);
+int mxfp4_stream_groups(int m, int k, int n, int cus, double tile_cost);
+int mxfp4_stream(const MgArgs &a, int groups, hipStream_t s);
 
 }  // namespace bqm

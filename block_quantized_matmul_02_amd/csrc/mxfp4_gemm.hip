@@ -11,7 +11,9 @@
 //    is left of a round of those: 128 x 128 (large_columns).
 //  * Codes pass through LDS in stages of 256 k, double-buffered, in rows whose
 //    16-byte chunks are permuted against bank conflicts; the scales of 1024 k
-//    are staged at once, one row a thread.  A scale dword per lane and stage
+//    are staged at once, one row a thread, whose bytes may be unaligned (odd
+//    counts of blocks; loaded byte by byte they made 2137 x 7712 x 7399 take
+//    273 us instead of 137).  A scale dword per lane and stage
 //    from memory instead took a third of the time at 2048 x 8192 x 8192.
 //  * y is stored past the caches.
 //
@@ -56,7 +58,7 @@ __device__ __forceinline__ void mg_tile(int id, int mtiles, int ntiles, int &mt,
 }
 
 // WM x WN waves, each TM x TN tiles of 32 x 32 (tokens x weight rows).
-// SW: bytes of the loads that scale rows are aligned to (16, 4 or 1).
+// SW: scale rows are aligned to 16 bytes (16) or to nothing (1).
 template <int WM, int WN, int TM, int TN, int SW>
 __global__ __launch_bounds__(64 * WM * WN) void mxfp4_gemm_kernel(MgArgs a) {
     constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN, NT = 64 * WM * WN, ROWS = BM + BN;
@@ -126,18 +128,27 @@ __global__ __launch_bounds__(64 * WM * WN) void mxfp4_gemm_kernel(MgArgs a) {
 #pragma unroll
                     for (int e = 0; e < 4; e++) S.v[i][4 * q + e] = v[e];
                 }
+            } else if (b0 + 8 * kMgSuper <= nblk) {
+                // 32 bytes at any alignment; a row past the last takes the last's
+                const int64_t q0 = isA ? m0 + min((int64_t)rr, rowsA - 1) : n0 + min((int64_t)(rr - BM), rowsB - 1);
+                const uint8_t *const p = (isA ? a.xs : a.ws) + q0 * nblk + b0;
+#pragma unroll
+                for (int q = 0; q < 2; q++) {
+                    u32x4 v;
+                    __builtin_memcpy(&v, p + 16 * q, 16);
+#pragma unroll
+                    for (int e = 0; e < 4; e++) S.v[i][4 * q + e] = v[e];
+                }
             } else {
+                // the row's last few bytes
 #pragma unroll
                 for (int q = 0; q < 2 * kMgSuper; q++) {
-                    const int b = 4 * q;
-                    if constexpr (SW == 4) {
-                        S.v[i][q] = __builtin_amdgcn_raw_buffer_load_b32(r, b0 + b < nblk ? at + b : 0x80000000u, 0, 0);
-                    } else {
-                        S.v[i][q] = 0;
+                    S.v[i][q] = 0;
 #pragma unroll
-                        for (int e = 0; e < 4; e++)
-                            S.v[i][q] |= (unsigned)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
-                                             r, b0 + b + e < nblk ? at + b + e : 0x80000000u, 0, 0) << (8 * e);
+                    for (int e = 0; e < 4; e++) {
+                        const int b = 4 * q + e;
+                        S.v[i][q] |= (unsigned)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
+                                         r, b0 + b < nblk ? at + b : 0x80000000u, 0, 0) << (8 * e);
                     }
                 }
             }
@@ -272,11 +283,8 @@ static int launch_mg(MgArgs a, hipStream_t s) {
     a.mtiles = (a.m + BM - 1) / BM;
     a.ntiles = (a.n + BN - 1) / BN;
     const int64_t grid = (int64_t)a.mtiles * a.ntiles;
-    const int sw = scale_load(a.k / 32, a.ws, a.xs);
-    if (sw == 16)
+    if (scale_load(a.k / 32, a.ws, a.xs) == 16)
         hipLaunchKernelGGL((mxfp4_gemm_kernel<WM, WN, TM, TN, 16>), dim3((unsigned)grid), dim3(NT), 0, s, a);
-    else if (sw == 4)
-        hipLaunchKernelGGL((mxfp4_gemm_kernel<WM, WN, TM, TN, 4>), dim3((unsigned)grid), dim3(NT), 0, s, a);
     else
         hipLaunchKernelGGL((mxfp4_gemm_kernel<WM, WN, TM, TN, 1>), dim3((unsigned)grid), dim3(NT), 0, s, a);
     return launch_status();
@@ -285,29 +293,33 @@ static int launch_mg(MgArgs a, hipStream_t s) {
 // Estimated microseconds (measured at k = 4096, 5120 and 8192): the large tile
 // takes 1.2 per stage and 11 besides for each round of one per compute unit;
 // the small one, two to a compute unit, 0.65 and 1.2 for each that a compute
-// unit gets, or 0.8 and 2 if it gets a single one.
+// unit gets, or 0.56 and 6 if it gets a single one (k = 4096 15 us, 8192 24,
+// 16384 41, 17408 46).
 static double large_cost(int64_t rounds, int stages) { return rounds * (1.2 * stages + 11.0); }
 static double small_cost(int64_t each, int stages) {
-    return each == 0 ? 0.0 : each == 1 ? 0.8 * stages + 2.0 : each * (0.65 * stages + 1.2);
+    return each == 0 ? 0.0 : each == 1 ? 0.56 * stages + 6.0 : each * (0.65 * stages + 1.2);
 }
 
 static int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Columns of the output that the large tile takes, the small one taking the
 // rest: all, none, or as many whole rounds of large tiles as fit, whichever
-// is estimated to end first.
-static int large_columns(int m, int k, int n, int cus) {
+// is estimated to end first, at `best` us.
+static int large_columns(int m, int k, int n, int cus, double &best) {
     const int stages = (int)up(k, 1024) * 4;
     const int64_t mt = up(m, kMgLargeM), nt = up(n, kMgLargeN), rounds = mt * nt / cus;
     const int64_t whole = rounds * cus / mt * kMgLargeN;   // columns of the whole rounds
     auto small = [&](int64_t cols) { return small_cost(up(up(m, kMgSmall) * up(cols, kMgSmall), cus), stages); };
-    double best = small(n);
+    best = small(n);
     int cols = 0;
     if (rounds > 0 && whole < n && large_cost(rounds, stages) + small(n - whole) < best) {
         best = large_cost(rounds, stages) + small(n - whole);
         cols = (int)whole;
     }
-    if (large_cost(up(mt * nt, cus), stages) < best) cols = n;
+    if (large_cost(up(mt * nt, cus), stages) < best) {
+        best = large_cost(up(mt * nt, cus), stages);
+        cols = n;
+    }
     return cols;
 }
 
@@ -324,8 +336,14 @@ extern "C" int bqm_mxfp4_gemm(const uint8_t *w, const uint8_t *ws, const uint8_t
     if (up(m, kMgSmall) * up(n, kMgSmall) * 512 > 0x7FFFFFFFll) return BQM_EUNSUPPORTED;
     hipStream_t s = as_stream(stream);
     MgArgs a = {w, ws, xq, xs, y, n, m, k, n, 0, 0};
-    if (mxfp4_stream_applies(m, k, n)) return mxfp4_stream(a, s);
-    const int cols = large_columns(m, k, n, device_cus());
+    double cost;
+    const int cols = large_columns(m, k, n, device_cus(), cost);
+    // unaligned scale rows that end inside the last 32 bytes cost the tiles a
+    // round of byte loads (463 x 288 x 91 12 us, 1302 x 8672 x 335 37, where the
+    // estimate says 8 and 26)
+    if (k / 32 % (8 * kMgSuper) != 0 && scale_load(k / 32, ws, xs) != 16) cost += 8.0;
+    const int groups = mxfp4_stream_groups(m, k, n, device_cus(), cost);
+    if (groups > 0) return mxfp4_stream(a, groups, s);
     if (cols > 0) {
         a.n = cols;
         const int rc = launch_mg<2, 4, 3, 2>(a, s);

@@ -1,5 +1,8 @@
 // The MXFP4 x MXFP4 product for few tokens (up to 64, as long as their codes
-// fit in registers or LDS): HBM-bound, every weight read once.
+// fit in registers or LDS): HBM-bound, every weight read once.  And for more
+// tokens in chunks, where the output has too few tiles for the other kernel to
+// fill the card: the waves share k (98 x 12512 x 320 12 us against 47, 512 x
+// 17408 x 512 27 against 46).
 //
 //  * Up to k = 4096 a wave has one 512-k slice of every tile and keeps the
 //    tokens' operand for it in registers.  Beyond, the workgroup keeps the
@@ -49,7 +52,7 @@ template <int G, int SW, bool XREG>
 __global__ __launch_bounds__(kMsWaves * 64, G == 1 && !XREG ? 4 : 2) void mxfp4_stream_kernel(MsArgs d) {
     constexpr int kAhead = 3;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    const MgArgs &a = d.a;
+    MgArgs a = d.a;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, g4 = lane >> 4;
@@ -58,6 +61,13 @@ __global__ __launch_bounds__(kMsWaves * 64, G == 1 && !XREG ? 4 : 2) void mxfp4_
     const int tiles = (a.n + 15) / 16;
     const int sub = wave / d.parts, wpart = wave % d.parts;   // with sub == subs: a wave without work
     const int hop = gridDim.x * d.subs;
+
+    // this workgroup's tokens
+    const int t0 = blockIdx.y * (16 * G);
+    a.m = a.m - t0 < 16 * G ? a.m - t0 : 16 * G;
+    a.xq += t0 * rb;
+    a.xs += (int64_t)t0 * nblk;
+    a.y += t0 * a.ldy;
 
     uint8_t *const xc = lds;                                              // [G][slices][4 steps][64 lanes][16]
     int *const xsc = reinterpret_cast<int *>(lds + G * d.slices * 4096);  // [G][slices][64 lanes]
@@ -259,8 +269,10 @@ static int launch_ms(MsArgs d, int cus, hipStream_t s) {
     d.per_wave = (d.slices + d.parts - 1) / d.parts;
     const int bytes = (int)ms_lds(XREG ? 0 : G, d.slices);
     const int units = (tiles + d.subs - 1) / d.subs;
-    const int most = cus * blocks_per_cu(cache, fn, kMsWaves * 64, bytes, 2);
-    hipLaunchKernelGGL((mxfp4_stream_kernel<G, SW, XREG>), dim3(units < most ? units : most), dim3(kMsWaves * 64), bytes, s, d);
+    const int chunks = (d.a.m + 16 * G - 1) / (16 * G);
+    int most = cus * blocks_per_cu(cache, fn, kMsWaves * 64, bytes, 2) / chunks;
+    if (most < 1) most = 1;
+    hipLaunchKernelGGL((mxfp4_stream_kernel<G, SW, XREG>), dim3(units < most ? units : most, chunks), dim3(kMsWaves * 64), bytes, s, d);
     return launch_status();
 }
 
@@ -279,16 +291,38 @@ static int launch_ms_g(const MgArgs &a, hipStream_t s) {
 // tiles; us): 16 x 4096 x 5152 8.0, 16.8, x 64448 30.2, 31.5; 32 x 4096 x 32768
 // 20.3, 21.8; 48 x 4096 x 20480 18.6, 18.9, x 32768 23.9, 23.1; 64 x 4096 x
 // 8192 14.2, 18.5, x 12288 17.6, 18.9, x 16384 19.9, 19.0.
-bool mxfp4_stream_applies(int m, int k, int n) {
+//
+// More tokens, or more than fit, go in chunks that each stream the weights
+// (again, from the caches): that fills the card where 128-row tiles are few and
+// k is long.  The chunks' estimated time decides, with a margin: 6 us, and for
+// each tile that a compute unit gets and each slice that a wave has of it the
+// time below.
+int mxfp4_stream_groups(int m, int k, int n, int cus, double tile_cost) {
     const int groups = (m + 15) / 16;
-    if (groups > kMsMaxGroups) return false;
-    const int rows = groups == 2 ? 128 : groups == 3 ? 80 : 48;   // of weights for a compute unit, at most
-    if (groups > 1 && n > rows * device_cus()) return false;
-    return k <= kMsWaves * 512 || ms_lds(groups, (int)(((int64_t)k + 511) / 512)) <= kMsLds;
+    auto fits = [&](int g) { return k <= kMsWaves * 512 || ms_lds(g, (int)(((int64_t)k + 511) / 512)) <= kMsLds; };
+    if (groups <= kMsMaxGroups && fits(groups)) {
+        const int rows = groups == 2 ? 128 : groups == 3 ? 80 : 48;   // of weights for a compute unit, at most
+        return groups == 1 || n <= rows * cus ? groups : 0;
+    }
+    const double in_registers[kMsMaxGroups] = {1.55, 1.75, 1.8, 2.4}, in_lds[kMsMaxGroups] = {1.1, 1.75, 2.5, 3.2};
+    const double *const item = k <= kMsWaves * 512 ? in_registers : in_lds;
+    const int slices = (int)(((int64_t)k + 511) / 512), parts = slices < kMsWaves ? slices : kMsWaves;
+    const int per_wave = (slices + parts - 1) / parts, subs = kMsWaves / parts;
+    const int64_t units = ((n + 15) / 16 + subs - 1) / subs;
+    int best = 0;
+    for (int g = 1; g <= kMsMaxGroups && g <= groups && fits(g); g++) {
+        const int64_t all = units * ((groups + g - 1) / g);
+        const double cost = 1.15 * (6.0 + (double)((all + cus - 1) / cus) * per_wave * item[g - 1]);
+        if (cost < tile_cost) {
+            tile_cost = cost;
+            best = g;
+        }
+    }
+    return best;
 }
 
-int mxfp4_stream(const MgArgs &a, hipStream_t s) {
-    switch ((a.m + 15) / 16) {
+int mxfp4_stream(const MgArgs &a, int groups, hipStream_t s) {
+    switch (groups) {
         case 1: return launch_ms_g<1>(a, s);
         case 2: return launch_ms_g<2>(a, s);
         case 3: return launch_ms_g<3>(a, s);

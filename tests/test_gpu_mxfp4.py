@@ -151,6 +151,23 @@ def test_gemm_matches_64_bits(bqm, m, k, n):
     check(y, ref, T, (3 * k / 64 + 2) * 2.0 ** -23, f"m={m} k={k} n={n}")
 
 
+# More tokens than one workgroup takes, against few weight rows: chunks of tokens, with a short last one.
+CHUNKS = [(65, 4096, 33), (98, 12512, 320), (63, 17088, 153), (130, 5120, 50), (200, 17408, 16), (129, 8192, 1), (257, 4128, 100),
+          (33, 16384, 70), (96, 10240, 257), (513, 17408, 40)]
+
+
+@pytest.mark.parametrize("m,k,n", CHUNKS)
+def test_gemm_few_rows_of_long_k(bqm, m, k, n):
+    rng = np.random.default_rng(m + 3 * k + n)
+    w, ws = random_mx(n, k, rng)
+    xq, xs = random_mx(m, k, rng)
+    y = torch.full((m + 2, n), float("nan"), device=DEV)
+    bqm.bqm_mxfp4_gemm(dev(w), dev(ws), dev(xq), dev(xs), y[1:m + 1])
+    ref, T = layer_ref.mxfp4_matmul(w, ws, layer_ref.mxfp4_values(xq, xs))
+    check(y[1:m + 1], ref, T, (3 * k / 64 + 2) * 2.0 ** -23, f"m={m} k={k} n={n}")
+    assert bool(torch.isnan(y[0]).all()) and bool(torch.isnan(y[m + 1]).all())
+
+
 @pytest.mark.parametrize("m,k,n", [(1, 512, 64), (40, 1024, 300), (300, 512, 300)])
 def test_gemm_wide_scales(bqm, m, k, n):
     """Scales 80 binades apart."""
