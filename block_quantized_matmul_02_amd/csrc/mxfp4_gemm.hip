@@ -13,16 +13,16 @@
 //    16-byte chunks are permuted against bank conflicts; the scales of 1024 k
 //    are staged at once, one row a thread, whose bytes may be unaligned (odd
 //    counts of blocks; loaded byte by byte they made 2137 x 7712 x 7399 take
-//    273 us instead of 137).  A scale dword per lane and stage
-//    from memory instead took a third of the time at 2048 x 8192 x 8192.
+//    273 us instead of 137).  A scale dword per lane and stage from memory
+//    instead took a third of the time at 2048 x 8192 x 8192.
 //  * y is stored past the caches.
 //
-// 512 x 4096 x 20480: 34.4 us (2.5 PFLOP/s); 3001 x 5120 x 17408: 169 us (3.2
-// PFLOP/s), the matrix cores busy 40% and 45% of the compute units' time.  2048
-// x 8192 x 8192 takes 111 us (2.5 PFLOP/s), and 57 (4.8) with every load and
-// LDS read taken out, on constant operands: what the matrix cores leave is the
-// operands' way through LDS and the stores, which a workgroup does not overlap
-// with its next tile.
+// 512 x 4096 x 20480: 34 to 39 us (2.5 PFLOP/s at best); 3001 x 5120 x 17408:
+// 167 to 174 us (3.2), the matrix cores busy 40% and 45% of the compute units'
+// time.  2048 x 8192 x 8192 takes 111 us (2.5 PFLOP/s), and 57 (4.8) with every
+// load and LDS read taken out, on constant operands: what the matrix cores
+// leave is the operands' way through LDS and the stores, which a workgroup does
+// not overlap with its next tile.
 #include <type_traits>
 
 #include "mxfp4.h"
