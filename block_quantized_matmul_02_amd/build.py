@@ -5,9 +5,9 @@ shared library next to this file.  Flags:
   -ffp-contract=off   floating-point contraction only where a kernel writes
                       an explicit fma, so results do not depend on inlining;
   -packed-fp32-ops    removed from the target features: no packed f32 VALU;
-  -amdgpu-mfma-vgpr-form=1 (MMQ only)
-                      MFMA sources and results in ordinary VGPRs, so the
-                      VALU fold reads the int32 block sums without copies.
+  -amdgpu-mfma-vgpr-form=1 (the sources in EXTRA)
+                      MFMA sources and results in ordinary VGPRs, so that
+                      the VALU reads the results without copies.
 """
 from __future__ import annotations
 
