@@ -24,13 +24,13 @@
 // columns are split over workgroups and a second, one-wave launch joins their
 // sums and lists.  512 x 131071 f32 with 5 alternatives: 54 us (4.9 TB/s); one
 // row of 64448 with 20: 8.3 us and 4.3 for the join, latency and sorting.
+#include "logprobs_keys.h"
 #include "values.h"
 
 namespace bqm {
 
 constexpr int kLpThreads = 256;
 constexpr int kLpWaves = kLpThreads / 64;
-constexpr int kLpVals = 16;                         // logits per thread and step
 constexpr int kLpStep = kLpThreads * kLpVals;       // logits per workgroup and step
 constexpr int kLpMaxSplits = 64;                    // a lane for each in the joining launch
 constexpr int kLpWantGroups = 512;                  // workgroups that fill the card: 2 per compute unit
@@ -50,23 +50,7 @@ struct LpArgs {
     int n_tokens, top, m, n, splits;
 };
 
-typedef unsigned long long u64;
-
 // ------------------------------------------------------------ keys and sorting
-
-// Whole numbers in the order of the values; -0 as +0, NaN below everything.
-__device__ __forceinline__ unsigned order_of(float v) {
-    const unsigned u = __builtin_bit_cast(unsigned, v + 0.0f);
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0;
-    return (u >> 31) ? ~u : u | 0x80000000u;
-}
-
-__device__ __forceinline__ float value_of(unsigned order) {
-    if (order == 0) return __builtin_nanf("");
-    return __builtin_bit_cast(float, (order >> 31) ? order & 0x7FFFFFFFu : ~order);
-}
-
-__device__ __forceinline__ u64 key_of(float v, int column) { return ((u64)order_of(v) << 32) | (unsigned)~column; }
 
 // The value of lane l ^ M.
 template <int M>
@@ -141,12 +125,6 @@ __device__ __forceinline__ u64 from_lane(u64 v, int lane) {
     return ((u64)(unsigned)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32) |
            (unsigned)__builtin_amdgcn_readlane((int)v, lane);
 }
-
-// Keys that can wait: fewer than a wave of them, and what a step appends before
-// they are looked at: up to 16 of each lane that reaches the bound, at most K
-// lanes or, where the bound is a value, K - 1 above it and 8 equal to it.
-constexpr int kLpTies = 8;
-constexpr int kLpWaiting = 64 + (BQM_LOGPROBS_MAX_TOP + kLpTies) * kLpVals;
 
 // One wave's best keys so far: 64 sorted in registers (none before the first
 // merge), and more in LDS that are above the bound and wait.
@@ -371,25 +349,22 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LpArgs a) {
             };
             best.raise(others);
             const u64 before = best.bound;
-            const bool open = (before >> 32) == 0;   // no bound, or one whose value is NaN
-            // columns past the bound's own lose ties against it
-            const float low0 = value_of((unsigned)(before >> 32));
-            const bool strict = st * kLpStep + wave * (64 * kLpVals) - skip > (int)~(unsigned)before;
-            const u64 above = __ballot(big >= kLowest && (open || big > low0 || (!strict && big == low0)));
+            const LpGate gate(before, st * kLpStep + wave * (64 * kLpVals) - skip);
+            const u64 above = __ballot(gate.admits(big));
             most = fmaxf(most, big);
-            if (!open && above == 0) return;
+            if (above == 0) return;   // whatever the order of the waves
             // The K-th of the lanes' running maxima is a bound, which all of its
             // value pass; keys decide where many lanes are equal to it.  Looked
             // for when K lanes pass at once and after every 8 + K / 2 that pass:
             // the sort costs as much as appending a few keys.
             const int lanes = __popcll(above);
             passed += lanes;
-            if (open || lanes >= a.top || passed >= 8 + a.top / 2) {
+            if (gate.open || lanes >= a.top || passed >= 8 + a.top / 2) {
                 passed = 0;
                 const float kth = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sort64f(most)), a.top - 1));
                 if (kth >= kLowest && __popcll(__ballot(most == kth)) <= kLpTies)
                     best.raise(((u64)order_of(kth) << 32) - 1);
-                else if (open || lanes >= a.top)
+                else if (gate.open || lanes >= a.top)
                     raise_by_keys();
             }
             // Append what passes: in one go where many lanes have something, else
