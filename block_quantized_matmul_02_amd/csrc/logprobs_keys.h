@@ -32,15 +32,20 @@ __host__ __device__ __forceinline__ u64 key_of(float v, int column) { return ((u
 // logit (NaN dropped; NaN where it has nothing else).  Every lane that holds one
 // has to be among them: the waves share their bounds and nothing orders their
 // steps, so a bound's column may be past the step's, at any value, -inf too.
+// Compared as the keys are, in whole numbers: a bound just below +0 stands for
+// -0 as a float, which is no less than +0.
 struct LpGate {
-    float low;     // the bound's value
-    bool open;     // no bound, or one whose value is NaN: every lane may
-    bool strict;   // the step's columns are past the bound's and lose ties against it
+    unsigned order;   // of the bound's value
+    bool open;        // no bound, or one whose value is NaN: every lane may
+    bool strict;      // the step's columns are past the bound's and lose ties against it
 
     __host__ __device__ __forceinline__ LpGate(u64 bound, int first_column)
-        : low(value_of((unsigned)(bound >> 32))), open((bound >> 32) == 0), strict(first_column > (int)~(unsigned)bound) {}
+        : order((unsigned)(bound >> 32)), open(order == 0), strict(first_column > (int)~(unsigned)bound) {}
 
-    __host__ __device__ __forceinline__ bool admits(float big) const { return open || big > low || (!strict && big == low); }
+    __host__ __device__ __forceinline__ bool admits(float big) const {
+        const unsigned o = order_of(big);
+        return open || o > order || (!strict && o == order);
+    }
 };
 
 // Keys that can wait: fewer than a wave of them, and what a step appends before

@@ -48,3 +48,17 @@ def test_fewer_finite_logits_than_alternatives(bqm, m, n, top):
             row[rng.choice(n, 40, replace=False)] = math.nan
         rows.append(row)
     ids_are_exact(bqm, rows, top, f"{m}x{n}")
+
+
+@pytest.mark.parametrize("m,n", [(600, 12000), (6, 4096), (40, 70000)])
+@pytest.mark.parametrize("top", range(1, 9))
+def test_ties_at_zero(bqm, m, n, top):
+    """All negative but for 2..8 zeros of both signs, anywhere in the row."""
+    rng = np.random.default_rng(n + top)
+    rows = []
+    for t in range(m):
+        row = -1.0 - rng.integers(0, 64, n) / 64.0
+        count = rng.integers(2, 9)
+        row[rng.choice(min(n, 20000), count, replace=False)] = np.where(rng.random(count) < 0.5, 0.0, -0.0)
+        rows.append(row)
+    ids_are_exact(bqm, rows, top, f"{m}x{n}")

@@ -84,3 +84,23 @@ def test_masks_that_leave_fewer_than_top(orders, top):
         orders(row, top)
         row[start:start + 3] = np.finfo(np.float32).min
         orders(row, top, 2, 8)
+
+
+def few_zeros(count, seed):
+    """Negative logits but for `count` zeros of both signs, in different waves of the same and of neighbouring steps."""
+    rng = np.random.default_rng(seed)
+    row = -1.0 - rng.random(N)
+    row[rng.choice(N, count, replace=False)] = np.where(rng.random(count) < 0.5, 0.0, -0.0)
+    return row
+
+
+@pytest.mark.parametrize("top", range(1, 9))
+def test_alternatives_that_tie_at_zero(orders, top):
+    """A bound just below +0 admits every zero of either sign, at the columns that win the tie too."""
+    for count in range(2, 9):
+        for seed in range(4):
+            orders(few_zeros(count, seed), top, count=100)
+    for tiny in (1e-45, -1e-45, 2e-38, -2e-38):          # and the neighbours of zero
+        row = few_zeros(6, top)
+        row[row == 0] = np.float32(tiny)
+        orders(row, top, count=100)
