@@ -1,0 +1,25 @@
+"""What the compiled kernels must not contain, read from the assembly that the build's own flags give (no GPU)."""
+import os
+import re
+import subprocess
+
+import pytest
+
+from block_quantized_matmul_02_amd import build
+
+
+def assembly(source):
+    cmd = [build.HIPCC, *build.HIPFLAGS, *build.EXTRA.get(source, []), "--cuda-device-only", "-S",
+           os.path.join(build.CSRC, source), "-o", "-"]
+    return subprocess.run(cmd, check=True, capture_output=True, text=True).stdout
+
+
+@pytest.fixture(scope="module")
+def logprobs():
+    return assembly("logprobs.hip")
+
+
+def test_the_waves_bound_is_read_from_lds(logprobs):
+    """An access that has lost its address space waits for every load in flight, the next steps' logits among them."""
+    assert "ds_max_u64" in logprobs                       # the bound's update
+    assert not re.findall(r"\bflat_(?:load|store|atomic)\w*", logprobs)
