@@ -27,6 +27,7 @@ namespace bqm {
 constexpr int kMsWaves = 8;
 constexpr int kMsMaxGroups = 4;             // of 16 tokens
 constexpr int kMsLds = 160 * 1024;
+constexpr int kMsMaxChunks = 65535;         // of tokens: workgroups along y
 
 struct MsArgs {
     MgArgs a;
@@ -311,7 +312,9 @@ int mxfp4_stream_groups(int m, int k, int n, int cus, double tile_cost) {
     const int64_t units = ((n + 15) / 16 + subs - 1) / subs;
     int best = 0;
     for (int g = 1; g <= kMsMaxGroups && g <= groups && fits(g); g++) {
-        const int64_t all = units * ((groups + g - 1) / g);
+        const int chunks = (groups + g - 1) / g;
+        if (chunks > kMsMaxChunks) continue;
+        const int64_t all = units * chunks;
         const double cost = 1.15 * (6.0 + (double)((all + cus - 1) / cus) * per_wave * item[g - 1]);
         if (cost < tile_cost) {
             tile_cost = cost;
