@@ -28,7 +28,7 @@ struct MxShape {
 
 template <typename T>
 __device__ __forceinline__ v8f load8(const T *p) {
-    return __builtin_convertvector(*reinterpret_cast<const typename Vec<T>::x8 *>(p), v8f);
+    return __builtin_convertvector(*reinterpret_cast<const typename Packed<T, 8, 16>::v *>(p), v8f);
 }
 
 template <typename T>
@@ -95,7 +95,8 @@ __global__ __launch_bounds__(kMxThreads) void mxfp4_dequantize_kernel(const unsi
         v[2 * e] = p[0] * s;
         v[2 * e + 1] = p[1] * s;
     }
-    __builtin_nontemporal_store(__builtin_convertvector(v, typename Vec<T>::x8), reinterpret_cast<typename Vec<T>::x8 *>(y + item * 8));
+    typedef T plain __attribute__((ext_vector_type(8)));
+    __builtin_nontemporal_store(__builtin_convertvector(v, plain), reinterpret_cast<typename Packed<T, 8, 16>::v *>(y + item * 8));
 }
 
 static bool mx_grid(int64_t items, unsigned *grid) {

@@ -63,7 +63,7 @@ struct Piece {
 template <typename T, int W, bool ALN>
 __device__ __forceinline__ auto load_piece(const T *p, int i, int k) {
     typedef float f __attribute__((ext_vector_type(W)));
-    typedef T tv __attribute__((ext_vector_type(W), aligned(ALN ? sizeof(T) * W : sizeof(T))));
+    typedef typename Packed<T, W, ALN ? 16 : sizeof(T)>::v tv;
     f v = {};
     if (i + W <= k) {
         v = __builtin_convertvector(*reinterpret_cast<const tv *>(p + i), f);
@@ -78,10 +78,10 @@ __device__ __forceinline__ auto load_piece(const T *p, int i, int k) {
 template <typename T, int W, bool ALN, typename F>
 __device__ __forceinline__ void store_piece(T *p, int i, int k, F v) {
     typedef T plain __attribute__((ext_vector_type(W)));
-    typedef T tv __attribute__((ext_vector_type(W), aligned(ALN ? sizeof(T) * W : sizeof(T))));
+    typedef typename Packed<T, W, ALN ? 16 : sizeof(T)>::v tv;
     if (i + W <= k) {
         if constexpr (ALN)
-            __builtin_nontemporal_store(__builtin_convertvector(v, plain), reinterpret_cast<plain *>(p + i));
+            __builtin_nontemporal_store(__builtin_convertvector(v, plain), reinterpret_cast<tv *>(p + i));
         else
             *reinterpret_cast<tv *>(p + i) = __builtin_convertvector(v, plain);
     } else if constexpr (!ALN) {

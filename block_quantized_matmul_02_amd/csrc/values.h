@@ -9,18 +9,11 @@ namespace bqm {
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v8f __attribute__((ext_vector_type(8)));
 
-template <typename T> struct Vec;
-template <> struct Vec<float> {
-    typedef float x4 __attribute__((ext_vector_type(4)));
-    typedef float x8 __attribute__((ext_vector_type(8)));
-};
-template <> struct Vec<_Float16> {
-    typedef _Float16 x4 __attribute__((ext_vector_type(4)));
-    typedef _Float16 x8 __attribute__((ext_vector_type(8)));
-};
-template <> struct Vec<__bf16> {
-    typedef __bf16 x4 __attribute__((ext_vector_type(4)));
-    typedef __bf16 x8 __attribute__((ext_vector_type(8)));
+// W values of T at an address aligned to A bytes; the vector's own alignment,
+// its whole size, may be more than the 16 bytes that pointers are checked for.
+template <typename T, int W, int A>
+struct Packed {
+    typedef T v __attribute__((ext_vector_type(W), aligned(A)));
 };
 
 // A buffer whose reads past `bytes` give zeros.
