@@ -121,9 +121,11 @@ __device__ __forceinline__ void emit(const NormArgs &a, int64_t t, int i, F y) {
         store_piece<T, W, ALN>(static_cast<T *>(a.y) + at, i, a.k, y);
         return;
     }
-    float big = 0.0f;
+    // from the first value, not from zero: a block of NaN alone keeps it, as in
+    // the quantizers (a NaN beside numbers is dropped)
+    float big = fabsf(y[0]);
 #pragma unroll
-    for (int e = 0; e < W; e++) big = fmaxf(big, fabsf(y[e]));
+    for (int e = 1; e < W; e++) big = fmaxf(big, fabsf(y[e]));
     words q;
     if constexpr (OUT == kOutQ81) {
         big = group_absmax<32 / W>(big);
