@@ -587,6 +587,7 @@ extern "C" int bqm_mxfp4_gemv(const uint8_t *w, const uint8_t *ws, const float *
     if (m < 1 || m > BQM_MXFP4_GEMV_MAX_M || k < 32 || n < 1) return BQM_EINVAL;
     if (k % 32 != 0 || !aligned(w, 16) || !aligned(x, 16) || !aligned(y, 4)) return BQM_EUNSUPPORTED;
     if (k > 1 << 24) return BQM_EUNSUPPORTED;   // 16 rows of x and of w in 31 bits
+    if (n > 0x7FFFFFFF - 2 * kMvRows) return BQM_EUNSUPPORTED;   // whole tiles, two at a time, in 31 bits
     MvArgs a = {w, ws, x, y, m, k, n, 0, 0, 0};
     const int slices = (k + kMvSlice - 1) / kMvSlice;
     a.passes = (slices + kMvMaxWaves - 1) / kMvMaxWaves;
