@@ -542,7 +542,8 @@ def bqm_logprobs_workspace(m: int, n: int, top_k: int) -> int:
     """Bytes of workspace that :func:`bqm_logprobs` needs for ``m`` rows of ``n`` logits."""
     size = lib().bqm_logprobs_workspace(m, n, top_k)
     if size < 0:
-        raise BqmError("bqm_logprobs_workspace", BQM_EINVAL)
+        valid = m >= 1 and n >= 1 and 0 <= top_k <= min(n, LOGPROBS_MAX_TOP)
+        raise BqmError("bqm_logprobs_workspace", BQM_EUNSUPPORTED if valid else BQM_EINVAL)
     return size
 
 

@@ -490,14 +490,17 @@ __global__ __launch_bounds__(64) void logprobs_join_kernel(LpArgs a) {
 // Splits of a row: enough workgroups to fill the card, each with at least one
 // whole step.  A function of the sizes alone, so that the workspace is too.
 static int lp_splits(int m, int n) {
-    const int steps = (n + kLpStep - 1) / kLpStep;
+    const int64_t steps = ((int64_t)n + kLpStep - 1) / kLpStep;
     int s = kLpWantGroups / m;
-    if (s > steps) s = steps;
+    if (s > steps) s = (int)steps;
     if (s > kLpMaxSplits) s = kLpMaxSplits;
     return s < 1 ? 1 : s;
 }
 
 static bool lp_sizes(int m, int n, int top) { return m >= 1 && n >= 1 && top >= 0 && top <= n && top <= BQM_LOGPROBS_MAX_TOP; }
+
+// A row's bytes in 31 bits, and the work items that a dispatch counts.
+static bool lp_fits(int m, int n) { return n <= kLpMaxN && (int64_t)m * kLpThreads <= 0xFFFFFFFFll; }
 
 template <typename T>
 static int launch_logprobs(const LpArgs &a, hipStream_t s) {
@@ -517,7 +520,7 @@ static int launch_logprobs(const LpArgs &a, hipStream_t s) {
 
 extern "C" int64_t bqm_logprobs_workspace(int m, int n, int top_k) {
     using namespace bqm;
-    if (!lp_sizes(m, n, top_k)) return -1;
+    if (!lp_sizes(m, n, top_k) || !lp_fits(m, n)) return -1;
     const int64_t splits = lp_splits(m, n);
     return splits == 1 ? 0 : m * splits * (int64_t)(sizeof(float4) + 8 * top_k);
 }
@@ -533,7 +536,7 @@ extern "C" int bqm_logprobs(const void *logits, int64_t ld, int type, const int 
     const int splits = lp_splits(m, n);
     if (splits > 1 && !workspace) return BQM_EINVAL;
     if (m > 1 && ld < n) return BQM_EUNSUPPORTED;
-    if (n > kLpMaxN || (int64_t)m * kLpThreads > 0xFFFFFFFFll) return BQM_EUNSUPPORTED;
+    if (!lp_fits(m, n)) return BQM_EUNSUPPORTED;
     if (!aligned(logits, type_bytes(type)) || !aligned(tokens, 4) || !aligned(logp, 4) || !aligned(lse, 4) ||
         !aligned(entropy, 4) || !aligned(top_ids, 4) || !aligned(top_logp, 4) || !aligned(workspace, 16))
         return BQM_EUNSUPPORTED;
