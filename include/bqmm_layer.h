@@ -103,7 +103,9 @@ int bqm_mxfp4_quantize(const void *x, int64_t ldx, uint8_t *codes, uint8_t *scal
 
 /*
  * bqm_mxfp4_dequantize: y[t][i] = 2^(s - 127) * e2m1(c), rounded once to
- * y_type (exact in f32 and, for normal results, in bf16).
+ * y_type: exact in f32 and, for normal results, in bf16, but for values past
+ * the type's range (in both from 4 at s = 253 and from 2 at s = 254), which
+ * become infinite.
  *   codes 4-byte aligned; y 16-byte aligned, dense; sizes as above.
  */
 int bqm_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, void *y, int y_type, int m, int k,
@@ -118,6 +120,11 @@ int bqm_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, void *y, i
  *   y      : f32 [m][n] out, 4-byte aligned.
  *   m, n >= 1, k >= 32 (else BQM_EINVAL); k % 32 == 0; w and xq 16-byte
  *   aligned (else BQM_EUNSUPPORTED).
+ * Any scales but 255 count, at each side up to 254: only their sum matters,
+ * and a result past the range of f32 is infinite (NaN where such infinities
+ * cancel).  A block with scale 255 makes its row or token NaN.  The order of
+ * the sums depends on the sizes, m too, so where sums round, a token's last
+ * bits may differ between calls of different m.
  */
 int bqm_mxfp4_gemm(const uint8_t *w, const uint8_t *ws, const uint8_t *xq, const uint8_t *xs, float *y, int m, int k,
                    int n, void *stream);

@@ -104,3 +104,19 @@ def test_gemm_scales_that_meet_their_opposite(bqm, m, k, total):
         rows = ((np.abs(ref) >= 2.0 ** -126) & (np.abs(ref) < 2.0 ** 127) | (ref == 0)).all(axis=0)
         assert rows.sum() > 40
         assert np.array_equal(y[:, rows], ref[:, rows].astype(np.float32)), f"scale {s}"
+
+
+@pytest.mark.parametrize("m,k", [(1, 512), (20, 1056), (700, 512)])
+def test_gemm_past_the_range(bqm, m, k):
+    """Products past f32's range are infinite with their sign, those inside it whole, and zero codes stay zero."""
+    w, ws = every_scale(k, 254, m)
+    at = np.random.default_rng(m).integers(0, k, m)
+    xq = np.zeros((m, k // 2), np.uint8)
+    xq[np.arange(m), at // 2] = 0x2 << (4 * (at % 2))                   # 1.0
+    xs = np.full((m, k // 32), 254, np.uint8)                           # times 2^127
+    y = bqm.bqm_mxfp4_gemm(dev(w), dev(ws), dev(xq), dev(xs)).cpu().numpy()
+    ref = 2.0 ** 127 * layer_ref.mxfp4_values(w, ws)[:, at].T
+    with np.errstate(over="ignore"):
+        want = ref.astype(np.float32)
+    assert np.isinf(want).any() and np.isfinite(want[ref != 0]).any()
+    assert np.array_equal(y, want)
