@@ -22,8 +22,9 @@
 //
 // HBM-bound (one read, the next two steps' loads in flight); with few rows the
 // columns are split over workgroups and a second, one-wave launch joins their
-// sums and lists.  512 x 131071 f32 with 5 alternatives: 54 us (4.9 TB/s); one
-// row of 64448 with 20: 8.3 us and 4.3 for the join, latency and sorting.
+// sums and lists.  512 x 131071 f32 with 5 alternatives: 52 us (5.2 TB/s); 300
+// rows of them 40 to 42 (3.8 TB/s: one workgroup a row); one row of 64448 with
+// 20: 7.3 us and 4.4 for the join, latency and sorting.
 #include "logprobs_keys.h"
 #include "values.h"
 

@@ -18,8 +18,11 @@
 //  * y is stored past the caches.
 //
 // 512 x 4096 x 20480: 34 to 39 us (2.5 PFLOP/s at best); 3001 x 5120 x 17408:
-// 167 to 174 us (3.2), the matrix cores busy 40% and 45% of the compute units'
-// time.  2048 x 8192 x 8192 takes 111 us (2.5 PFLOP/s), and 57 (4.8) with every
+// 167 to 178 us (3.2) a few at a time, 187 to 199 in long rows of calls, when
+// the clock falls, the matrix cores busy 40% and 46% of the compute units'
+// time.  Few tiles leave compute units idle (512 x 4096 x 4096, 128 tiles, 18.4
+// us), and k runs in whole groups of four stages (512 x 4128 x 20480 55 us).
+// 2048 x 8192 x 8192 takes 111 us (2.5 PFLOP/s), and 57 (4.8) with every
 // load and LDS read taken out, on constant operands: what the matrix cores
 // leave is the operands' way through LDS and the stores, which a workgroup does
 // not overlap with its next tile.

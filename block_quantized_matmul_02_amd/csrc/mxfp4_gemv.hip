@@ -28,7 +28,11 @@
 //  * The waves' partial tiles meet in LDS, added in wave order.
 //
 // Weights from HBM: 1 x 4096 x 4096 7.2 us (latency), 1 x 4096 x 64448 28.9 us
-// (4.9 TB/s), 9 x 4096 x 64448 32.8 us (4.3 TB/s), 5 x 17408 x 5120 28.5 us.
+// (4.9 TB/s), 9 x 4096 x 64448 32.8 us (4.3 TB/s), 5 x 17408 x 5120 28.1 us.
+// Long rows are further from the weights' time (1 x 17408 x 5120 24.1 us, 9.3
+// for its bytes): 320 tiles are two rounds of 256 workgroups, 34 slices five
+// turns of eight waves, and x is cut first.  G = 3 fills the registers and
+// spills 6 (11 with unaligned scales) to scratch: 16 x 4096 x 64448 43 us.
 #include "mxfp4.h"
 
 namespace bqm {

@@ -16,7 +16,8 @@
 //    has fewer than eight slices several tiles; parts meet in LDS, added in
 //    wave order.
 //
-// Weights from HBM: 16 x 4096 x 5152 8.0 us (latency: two tiles a workgroup),
+// Weights from HBM: 16 x 4096 x 5152 8.0 us (latency: at 136 registers one
+// workgroup a compute unit, so 66 of the 256 take a second of the 322 tiles),
 // 16 x 4096 x 64448 30.2 us (4.8 TB/s), 16 x 17408 x 20480 44 us (4.3 TB/s).
 #include <type_traits>
 
