@@ -2,8 +2,9 @@
 
 Argument marshalling only: every step runs in the HIP kernels of
 ``libbqmm.so`` (built in-tree by ``block_quantized_matmul_02_amd.build``).
-The functions carry the C ABI's names (``include/bqmm.h`` and, for the
-operators around the matmul, ``include/bqmm_layer.h``), take torch
+The functions carry the C ABI's names (``include/bqmm.h``, for the
+operators around the matmul ``include/bqmm_layer.h``, and for products whose
+weights differ from row to row ``include/bqmm_groups.h``), take torch
 tensors that live on the GPU, enqueue on torch's current stream and never
 synchronize.  There is no CPU fallback: a missing library raises.
 """
@@ -24,6 +25,11 @@ GEMV_MAX_M = 15
 E4M3_GEMV_MAX_M = 16
 MXFP4_GEMV_MAX_M = 16
 LOGPROBS_MAX_TOP = 32
+MAX_GROUPS = 1024
+MAX_TOP = 32
+EXPERT_GEMV_MAX_SLOTS = 256
+EXPERT_GEMV_MAX_K = 16384
+LORA_MAX_RANK = 256
 BQM_F32 = 0
 BQM_F16 = 1
 BQM_BF16 = 2
@@ -79,6 +85,19 @@ def lib() -> ctypes.CDLL:
         L.bqm_logprobs_workspace.restype = I64
         for fn in ("bqm_add_rmsnorm", "bqm_add_rmsnorm_q8_1", "bqm_add_rmsnorm_e4m3_blk", "bqm_mxfp4_quantize",
                    "bqm_mxfp4_dequantize", "bqm_mxfp4_gemm", "bqm_mxfp4_gemv", "bqm_logprobs"):
+            getattr(L, fn).restype = ctypes.c_int
+        L.bqm_route.argtypes = [P, I64, I, I, I, P, P, I, I, P]
+        L.bqm_group_rows.argtypes = [P, I, I, P, P, P, P]
+        L.bqm_group_rows_workspace.argtypes = [I, I]
+        L.bqm_mxfp4_grouped_gemm.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, P]
+        L.bqm_mxfp4_expert_gemv.argtypes = [P, P, P, P, P, I, I, I, I, I, I, P]
+        L.bqm_combine.argtypes = [P, I, P, P, P, I, I, I, I, P]
+        L.bqm_lora_add.argtypes = [P, I64, I, P, P, I, P, P, P, P, I64, P, I64, P, I, I, I, I, I, P]
+        L.bqm_lora_add_workspace.argtypes = [I, I]
+        L.bqm_group_rows_workspace.restype = I64
+        L.bqm_lora_add_workspace.restype = I64
+        for fn in ("bqm_route", "bqm_group_rows", "bqm_mxfp4_grouped_gemm", "bqm_mxfp4_expert_gemv", "bqm_combine",
+                   "bqm_lora_add"):
             getattr(L, fn).restype = ctypes.c_int
         L.bqm_strerror.argtypes = [I]
         L.bqm_strerror.restype = ctypes.c_char_p
@@ -586,3 +605,195 @@ def bqm_logprobs(logits, tokens=None, top_k: int = 0, out=None, workspace=None):
                                               _ptr(lse), _ptr(entropy), _ptr(ids), _ptr(top), top_k,
                                               _optr(workspace), m, n, _stream(logits)))
     return logp, lse, entropy, ids, top
+
+
+# ----------------------------- products whose weights differ from row to row
+
+
+def bqm_route(logits, top: int, renorm: bool = True, ids=None, weights=None):
+    """Each token's ``top`` experts of ``logits [m, e]`` (f32, fp16 or bf16, any row stride) -> (int32
+    ``ids [m, top]``, f32 ``weights [m, top]``): the largest first, the lowest column first among equals.
+
+    The weights are the softmax over all columns, or with ``renorm`` over the chosen.  A logit of -inf or NaN is never
+    chosen; where fewer than ``top`` are left the last ids are -1 with weight 0.
+    """
+    import torch
+
+    ld = _rows(logits, "logits")
+    m, e = logits.shape
+    if ids is None:
+        ids = torch.empty((m, max(top, 0)), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((m, max(top, 0)), dtype=torch.float32, device=logits.device)
+    _check(ids, torch.int32, "ids", (m, max(top, 0)))
+    _check(weights, torch.float32, "weights", (m, max(top, 0)))
+    _raise("bqm_route", lib().bqm_route(_ptr(logits), ld, _type(logits, "logits"), top, 1 if renorm else 0, _ptr(ids),
+                                        _ptr(weights), m, e, _stream(logits)))
+    return ids, weights
+
+
+@functools.lru_cache(maxsize=256)
+def bqm_group_rows_workspace(count: int, groups: int) -> int:
+    """Bytes of workspace that :func:`bqm_group_rows` needs for ``count`` rows and ``groups`` groups."""
+    size = lib().bqm_group_rows_workspace(count, groups)
+    if size < 0:
+        raise BqmError("bqm_group_rows_workspace", BQM_EINVAL)
+    return size
+
+
+def _workspace(workspace, need, device):
+    """The caller's workspace, checked, or a new one; None if none is needed."""
+    import torch
+
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    _check(workspace, torch.uint8, "workspace")
+    if workspace.numel() < need:
+        raise ValueError(f"workspace must hold {need} bytes, got {workspace.numel()}")
+    return workspace
+
+
+def bqm_group_rows(ids, groups: int, offsets=None, order=None, workspace=None):
+    """Rows sorted by their group, those of a group in their own order: int32 ``ids`` (any shape, taken flat) ->
+    (int32 ``offsets [groups + 1]``, int32 ``order [ids.numel()]``).
+
+    Rows whose id is outside 0..groups-1 stand behind the last group.  ``workspace`` is uint8 of at least
+    :func:`bqm_group_rows_workspace` bytes.
+    """
+    import torch
+
+    count = ids.numel()
+    _check(ids, torch.int32, "ids")
+    need = bqm_group_rows_workspace(count, groups)
+    if offsets is None:
+        offsets = torch.empty(groups + 1, dtype=torch.int32, device=ids.device)
+    if order is None:
+        order = torch.empty(count, dtype=torch.int32, device=ids.device)
+    _check(offsets, torch.int32, "offsets", (groups + 1,))
+    _check(order, torch.int32, "order", (count,))
+    workspace = _workspace(workspace, need, ids.device)
+    _raise("bqm_group_rows", lib().bqm_group_rows(_ptr(ids), count, groups, _ptr(offsets), _ptr(order), _optr(workspace),
+                                                  _stream(ids)))
+    return offsets, order
+
+
+def _experts(w, ws):
+    """The sizes (groups, n, k) of experts' weights, checked."""
+    import torch
+
+    if w.dim() != 3:
+        raise ValueError(f"w must be [groups, n, k/2], got {tuple(w.shape)}")
+    groups, n, half = w.shape
+    _check(w, torch.uint8, "w")
+    _check(ws, torch.uint8, "ws", (groups, n, half // 16))
+    return groups, n, 2 * half
+
+
+def bqm_mxfp4_grouped_gemm(w, ws, xq, xs, offsets, order, glu: bool = False, out_dtype=None, y=None):
+    """MXFP4 x MXFP4 GEMM whose weights depend on the slot's group: ``w [groups, n, k/2]``, ``ws [groups, n, k/32]``,
+    activations ``xq [rows, k/2]``, ``xs [rows, k/32]`` -> ``y [slots, n]``, slots = ``order.numel()``.
+
+    ``offsets [groups + 1]`` and ``order [slots]`` are :func:`bqm_group_rows`' of the slots' ids; slot s takes row
+    ``s // (slots // rows)``.  With ``glu`` the first half of the weight rows is a gate: ``y [slots, n / 2]`` =
+    silu(gate) * other half.  y is f32, fp16 or bf16 (``out_dtype``, f32 if not given); a slot of no group gets zeros.
+    """
+    import torch
+
+    groups, n, k = _experts(w, ws)
+    rows, slots = xq.shape[0], order.numel()
+    _check(xq, torch.uint8, "xq", (rows, k // 2))
+    _check(xs, torch.uint8, "xs", (rows, k // 32))
+    _check(offsets, torch.int32, "offsets", (groups + 1,))
+    _check(order, torch.int32, "order", (slots,))
+    outs = n // 2 if glu else n
+    if y is None:
+        y = torch.empty((slots, outs), dtype=out_dtype or torch.float32, device=xq.device)
+    _check(y, out_dtype or y.dtype, "y", (slots, outs))
+    _raise("bqm_mxfp4_grouped_gemm",
+           lib().bqm_mxfp4_grouped_gemm(_ptr(w), _ptr(ws), _ptr(xq), _ptr(xs), _ptr(offsets), _ptr(order), _ptr(y),
+                                        _type(y, "y"), 1 if glu else 0, rows, slots, groups, k, n, _stream(w)))
+    return y
+
+
+def bqm_mxfp4_expert_gemv(w, ws, x, ids, glu: bool = False, y=None):
+    """The decode / verify form of :func:`bqm_mxfp4_grouped_gemm`, at most 256 slots: f32 ``x [rows, k]`` and the slots'
+    int32 ``ids`` (any shape, taken flat, as :func:`bqm_route` gives them) -> f32 ``y [slots, n or n / 2]``."""
+    import torch
+
+    groups, n, k = _experts(w, ws)
+    rows, slots = x.shape[0], ids.numel()
+    _check(x, torch.float32, "x", (rows, k))
+    _check(ids, torch.int32, "ids")
+    outs = n // 2 if glu else n
+    if y is None:
+        y = torch.empty((slots, outs), dtype=torch.float32, device=x.device)
+    _check(y, torch.float32, "y", (slots, outs))
+    _raise("bqm_mxfp4_expert_gemv", lib().bqm_mxfp4_expert_gemv(_ptr(w), _ptr(ws), _ptr(x), _ptr(ids), _ptr(y),
+                                                                1 if glu else 0, rows, slots, groups, k, n, _stream(w)))
+    return y
+
+
+def bqm_combine(y, weights, res=None, out=None, out_dtype=None):
+    """The weighted sum of each token's slots: ``y [m * top, n]`` (f32, fp16 or bf16) and f32 ``weights [m, top]`` ->
+    ``out [m, n]`` = (``res`` +) sum_j weights[:, j] * y[:, j].
+
+    out and res are f32 or y's type alike (``out_dtype``, res' type or else f32 if not given); out may be res.
+    """
+    import torch
+
+    m, top = weights.shape
+    n = y.shape[1]
+    _check(y, y.dtype, "y", (m * top, n))
+    _check(weights, torch.float32, "weights")
+    if out is None:
+        out = torch.empty((m, n), dtype=out_dtype or (torch.float32 if res is None else res.dtype), device=y.device)
+    _check(out, out_dtype or out.dtype, "out", (m, n))
+    if res is not None:
+        _check(res, out.dtype, "res", (m, n))
+    _raise("bqm_combine", lib().bqm_combine(_ptr(y), _type(y, "y"), _ptr(weights), _optr(res), _ptr(out),
+                                            _type(out, "out"), m, top, n, _stream(y)))
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def bqm_lora_add_workspace(m: int, r: int) -> int:
+    """Bytes of workspace that :func:`bqm_lora_add` needs for ``m`` rows and adapters of rank ``r``."""
+    size = lib().bqm_lora_add_workspace(m, r)
+    if size < 0:
+        raise BqmError("bqm_lora_add_workspace", BQM_EINVAL)
+    return size
+
+
+def bqm_lora_add(x, a, b, offsets, order, scale=None, res=None, y=None, workspace=None):
+    """Low-rank adapters beside a projection: ``a [adapters, r, k]``, ``b [adapters, n, r]`` (fp16 or bf16 alike) and
+    ``x [m, k]`` (f32 or their type, any row stride) -> f32 ``y [m, n]`` = (``res`` +) scale[e] * B[e] (A[e] x) for a
+    row of adapter e, ``res`` or zeros for a row of none.
+
+    ``offsets [adapters + 1]`` and ``order [m]`` are :func:`bqm_group_rows`' of the rows' adapters; ``scale`` is f32
+    ``[adapters]`` or None for ones.  ``res`` is the projection's f32 output, any row stride, and y may be it.
+    ``workspace`` is uint8 of at least :func:`bqm_lora_add_workspace` bytes.
+    """
+    import torch
+
+    ldx = _rows(x, "x")
+    m, k = x.shape
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError(f"a and b must be [adapters, r, k] and [adapters, n, r], got {tuple(a.shape)} and {tuple(b.shape)}")
+    adapters, r, _ = a.shape
+    n = b.shape[1]
+    _check(a, a.dtype, "a", (adapters, r, k))
+    _check(b, a.dtype, "b", (adapters, n, r))
+    _check(offsets, torch.int32, "offsets", (adapters + 1,))
+    _check(order, torch.int32, "order", (m,))
+    if scale is not None:
+        _check(scale, torch.float32, "scale", (adapters,))
+    ldr = 0 if res is None else _rows(res, "res", torch.float32, (m, n))
+    if y is None:
+        y = torch.empty((m, n), dtype=torch.float32, device=x.device)
+    ldy = _rows(y, "y", torch.float32, (m, n))
+    workspace = _workspace(workspace, bqm_lora_add_workspace(m, r), x.device)
+    _raise("bqm_lora_add",
+           lib().bqm_lora_add(_ptr(x), ldx, _type(x, "x"), _ptr(a), _ptr(b), _type(a, "a"), _optr(scale), _ptr(offsets),
+                              _ptr(order), _optr(res), ldr, _ptr(y), ldy, _ptr(workspace), m, k, n, r, adapters,
+                              _stream(x)))
+    return y

@@ -1,0 +1,79 @@
+// Shared by the kernels whose rows are grouped by an index on the device.
+#pragma once
+
+#include "bqmm_groups.h"
+#include "values.h"
+
+namespace bqm {
+
+// The arguments through which rows are found.
+struct Grouping {
+    const int *offsets, *order;
+    int groups, slots;
+};
+
+// A workgroup's share of a group: `rows` sorted positions from `first` on, and
+// which of the group's tiles (local) it is.
+struct GroupTile {
+    int group;   // == groups: rows of no group; > groups: no work
+    int first, rows, local;
+};
+
+// Item `id` of the list in which every group has ceil(rows / bm) * mult items,
+// the rows of no group last.  A wave looks at 64 groups at a time; uniform.
+// Offsets are taken into 0..slots, so positions are always inside order.
+__device__ __forceinline__ GroupTile find_group(const Grouping &q, int bm, int mult, int id) {
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+    for (int base = 0; base <= q.groups; base += 64) {
+        const int g = base + lane;
+        const int lo = g <= q.groups ? min(max(q.offsets[g], 0), q.slots) : q.slots;
+        const int hi = g < q.groups ? min(max(q.offsets[g + 1], 0), q.slots) : q.slots;
+        const int rows = max(hi - lo, 0);
+        const int items = (rows + bm - 1) / bm * mult;
+        int upto = items;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int other = __shfl_up(upto, d);
+            if (lane >= d) upto += other;
+        }
+        const uint64_t past = __ballot(before + upto > id);
+        if (past != 0) {
+            const int at = __builtin_ctzll(past);
+            GroupTile t;
+            t.group = base + at;
+            t.local = id - before - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(items, at));
+            t.first = __builtin_amdgcn_readlane(lo, at);
+            t.rows = __builtin_amdgcn_readlane(rows, at);
+            return t;
+        }
+        before += __builtin_amdgcn_readlane(upto, 63);
+    }
+    return GroupTile{q.groups + 1, 0, 0, 0};
+}
+
+// The most tiles of bm rows that `slots` rows of `groups` groups (and of none) make.
+inline int64_t most_tiles(int slots, int groups, int bm) {
+    return (int64_t)slots / bm + (slots < groups + 1 ? slots : groups + 1);
+}
+
+// f32 -> type, stored.
+__device__ __forceinline__ void store_as(void *p, int64_t i, float v, int type) {
+    if (type == BQM_F32)
+        static_cast<float *>(p)[i] = v;
+    else if (type == BQM_F16)
+        static_cast<_Float16 *>(p)[i] = (_Float16)v;
+    else
+        static_cast<__bf16 *>(p)[i] = (__bf16)v;
+}
+
+__device__ __forceinline__ float load_as(const void *p, int64_t i, int type) {
+    if (type == BQM_F32) return static_cast<const float *>(p)[i];
+    if (type == BQM_F16) return (float)static_cast<const _Float16 *>(p)[i];
+    return (float)static_cast<const __bf16 *>(p)[i];
+}
+
+// x / (1 + exp(-x)).
+__device__ __forceinline__ float silu(float x) { return x / (1.0f + expf(-x)); }
+
+}  // namespace bqm

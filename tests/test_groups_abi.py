@@ -1,0 +1,164 @@
+"""C-ABI checks of include/bqmm_groups.h that need no GPU: the library exports what the header declares and
+rejects bad arguments before any HIP call; the binding refuses tensors that do not fit."""
+import ctypes
+import os
+import re
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "bqmm_groups.h")
+
+P = ctypes.c_void_p
+A, B, C, D, E, G, H = (P(i << 20) for i in range(1, 8))   # aligned stand-ins; never dereferenced
+ODD = P(0x100001)
+MIS2 = P(0x100002)
+MIS4 = P(0x100004)
+MIS8 = P(0x100008)
+NUL = P(0)
+
+
+@pytest.fixture(scope="module")
+def L():
+    import block_quantized_matmul_02_amd as bqm
+
+    if not os.path.exists(bqm.LIB_PATH):
+        from block_quantized_matmul_02_amd import build
+
+        build.build()
+    return bqm.lib()
+
+
+def test_library_exports_every_declared_symbol(L):
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = sorted(set(re.findall(r"\b(bqm_\w+)\s*\(", text)))
+    assert names == sorted(["bqm_route", "bqm_group_rows", "bqm_group_rows_workspace", "bqm_mxfp4_grouped_gemm",
+                            "bqm_mxfp4_expert_gemv", "bqm_combine", "bqm_lora_add", "bqm_lora_add_workspace"])
+    for name in names:
+        assert hasattr(L, name), name
+
+
+def test_header_compiles_as_c(tmp_path):
+    src = tmp_path / "t.c"
+    src.write_text('#include "bqmm_groups.h"\nint main(void) { return BQM_MAX_GROUPS == 1024 ? 0 : 1; }\n')
+    assert os.system(f"gcc -std=c99 -Wall -Werror -fsyntax-only -I {os.path.dirname(HEADER)} {src}") == 0
+
+
+def test_constants_match_the_header():
+    import block_quantized_matmul_02_amd as bqm
+
+    text = open(HEADER).read()
+    for name in ("MAX_GROUPS", "MAX_TOP", "EXPERT_GEMV_MAX_SLOTS", "EXPERT_GEMV_MAX_K", "LORA_MAX_RANK"):
+        assert int(re.search(rf"#define BQM_{name} (\d+)", text).group(1)) == getattr(bqm, name), name
+
+
+def test_route_validation(L):
+    def f(l=A, ld=64, t=0, top=4, renorm=1, ids=B, w=C, m=2, e=64):
+        return L.bqm_route(l, ld, t, top, renorm, ids, w, m, e, NUL)
+
+    assert f(l=NUL) == 1 and f(ids=NUL) == 1 and f(w=NUL) == 1 and f(t=3) == 1 and f(t=-1) == 1
+    assert f(m=0) == 1 and f(e=0) == 1 and f(e=1025, ld=1025) == 1
+    assert f(top=0) == 1 and f(top=33) == 1 and f(top=5, e=4) == 1 and f(top=-1) == 1
+    assert f(ld=63) == 2 and f(l=MIS2) == 2 and f(t=1, l=ODD) == 2 and f(ids=MIS2) == 2 and f(w=MIS2) == 2
+    assert f(m=2 ** 31 - 1) == 2
+
+
+def test_group_rows_validation(L):
+    def f(ids=A, count=10, groups=4, off=B, order=C, ws=NUL):
+        return L.bqm_group_rows(ids, count, groups, off, order, ws, NUL)
+
+    assert f(ids=NUL) == 1 and f(off=NUL) == 1 and f(order=NUL) == 1
+    assert f(count=0) == 1 and f(count=(1 << 30) + 1) == 1 and f(groups=0) == 1 and f(groups=1025) == 1
+    assert f(count=100000) == 1                              # needs a workspace
+    assert f(ids=MIS2) == 2 and f(off=MIS2) == 2 and f(order=MIS2) == 2 and f(count=100000, ws=MIS2) == 2
+    size = L.bqm_group_rows_workspace
+    assert size(0, 4) == -1 and size(10, 0) == -1 and size(10, 1025) == -1 and size((1 << 30) + 1, 4) == -1
+    assert size(1, 1) == 0 and size(64, 1024) == 0 and size(100000, 256) > 0 and size(1 << 30, 1024) > 0
+
+
+@pytest.mark.parametrize("glu", [0, 1])
+def test_grouped_gemm_validation(L, glu):
+    def f(w=A, ws=B, xq=C, xs=D, off=E, order=G, y=H, yt=0, rows=2, slots=4, groups=3, k=64, n=8):
+        return L.bqm_mxfp4_grouped_gemm(w, ws, xq, xs, off, order, y, yt, glu, rows, slots, groups, k, n, NUL)
+
+    for name in ("w", "ws", "xq", "xs", "off", "order", "y"):
+        assert f(**{name: NUL}) == 1, name
+    assert f(yt=3) == 1 and f(rows=0) == 1 and f(slots=0) == 1 and f(slots=5) == 1 and f(rows=4, slots=2) == 1
+    assert f(groups=0) == 1 and f(groups=1025) == 1 and f(k=16) == 1 and f(n=0) == 1
+    assert f(k=48) == 2 and f(w=MIS8) == 2 and f(xq=MIS8) == 2
+    assert f(off=MIS2) == 2 and f(order=MIS2) == 2 and f(y=MIS2) == 2 and f(yt=1, y=ODD) == 2
+    assert f(rows=2 ** 30, slots=2 ** 30, n=2 ** 20) == 2    # more tiles than a dispatch counts
+    if glu:
+        assert f(n=7) == 1
+
+
+@pytest.mark.parametrize("glu", [0, 1])
+def test_expert_gemv_validation(L, glu):
+    def f(w=A, ws=B, x=C, ids=D, y=E, rows=2, slots=4, groups=3, k=64, n=8):
+        return L.bqm_mxfp4_expert_gemv(w, ws, x, ids, y, glu, rows, slots, groups, k, n, NUL)
+
+    for name in ("w", "ws", "x", "ids", "y"):
+        assert f(**{name: NUL}) == 1, name
+    assert f(rows=0) == 1 and f(slots=0) == 1 and f(slots=5) == 1 and f(rows=257, slots=257) == 1
+    assert f(groups=0) == 1 and f(groups=1025) == 1 and f(k=16) == 1 and f(n=0) == 1
+    assert f(k=48) == 2 and f(k=16384 + 32) == 2 and f(w=MIS8) == 2 and f(x=MIS8) == 2 and f(ids=MIS2) == 2 and f(y=MIS2) == 2
+    if glu:
+        assert f(n=7) == 1
+
+
+def test_combine_validation(L):
+    def f(y=A, yt=0, w=B, res=C, out=D, ot=0, m=2, top=4, n=8):
+        return L.bqm_combine(y, yt, w, res, out, ot, m, top, n, NUL)
+
+    assert f(y=NUL) == 1 and f(w=NUL) == 1 and f(out=NUL) == 1 and f(yt=3) == 1 and f(ot=-1) == 1
+    assert f(m=0) == 1 and f(n=0) == 1 and f(top=0) == 1 and f(top=33) == 1
+    assert f(yt=0, ot=1) == 2 and f(yt=1, ot=2) == 2
+    assert f(y=MIS2) == 2 and f(yt=1, y=ODD) == 2 and f(w=MIS2) == 2 and f(res=MIS2) == 2 and f(out=MIS2) == 2
+    assert f(m=2 ** 31 - 1, n=2 ** 20) == 2
+
+
+def test_lora_add_validation(L):
+    def f(x=A, ldx=64, xt=0, a=B, b=C, abt=2, scale=D, off=E, order=G, res=H, ldr=8, y=A, ldy=8, ws=B, m=2, k=64, n=8,
+          r=16, ad=3):
+        return L.bqm_lora_add(x, ldx, xt, a, b, abt, scale, off, order, res, ldr, y, ldy, ws, m, k, n, r, ad, NUL)
+
+    for name in ("x", "a", "b", "off", "order", "y", "ws"):
+        assert f(**{name: NUL}) == 1, name
+    assert f(xt=3) == 1 and f(abt=3) == 1 and f(m=0) == 1 and f(k=0) == 1 and f(n=0) == 1
+    assert f(r=0) == 1 and f(r=264) == 1 and f(ad=0) == 1 and f(ad=1025) == 1
+    assert f(abt=0) == 2 and f(xt=1, abt=2) == 2 and f(xt=2, abt=1) == 2 and f(k=60) == 2 and f(r=12) == 2
+    assert f(ldx=56) == 2 and f(ldx=66) == 2 and f(xt=2, ldx=68) == 2 and f(ldr=7) == 2 and f(ldy=7) == 2
+    assert f(x=MIS8) == 2 and f(a=MIS8) == 2 and f(b=MIS8) == 2 and f(ws=MIS8) == 2
+    assert f(scale=MIS2) == 2 and f(off=MIS2) == 2 and f(order=MIS2) == 2 and f(res=MIS2) == 2 and f(y=MIS2) == 2
+    assert f(res=A, ldr=8, y=A, ldy=16) == 2                 # in place: the same rows
+    size = L.bqm_lora_add_workspace
+    assert size(0, 16) == -1 and size(1, 0) == -1 and size(1, 257) == -1 and size(3, 16) > 0
+    assert size(2 ** 31 - 1, 256) > 2 ** 31
+
+
+def test_binding_refuses_what_does_not_fit():
+    """Host tensors stand for any tensor that is not on a GPU."""
+    torch = pytest.importorskip("torch")
+    import block_quantized_matmul_02_amd as bqm
+
+    i = torch.zeros(4, dtype=torch.int32)
+    u = torch.zeros((2, 4, 16), dtype=torch.uint8)
+    f = torch.zeros((2, 32))
+    with pytest.raises(ValueError):
+        bqm.bqm_route(f, 2)
+    with pytest.raises(ValueError):
+        bqm.bqm_group_rows(i, 4)
+    with pytest.raises(ValueError):
+        bqm.bqm_mxfp4_grouped_gemm(u, u, u[0], u[0], i, i)
+    with pytest.raises(ValueError):
+        bqm.bqm_mxfp4_grouped_gemm(u[0], u, u[0], u[0], i, i)
+    with pytest.raises(ValueError):
+        bqm.bqm_mxfp4_expert_gemv(u, u, f, i)
+    with pytest.raises(ValueError):
+        bqm.bqm_combine(f, f)
+    with pytest.raises(ValueError):
+        bqm.bqm_lora_add(f, u.half(), u.half(), i, i)
+    with pytest.raises(bqm.BqmError):
+        bqm.bqm_group_rows_workspace(0, 4)
+    with pytest.raises(bqm.BqmError):
+        bqm.bqm_lora_add_workspace(4, 1000)
