@@ -73,7 +73,23 @@ __device__ __forceinline__ float load_as(const void *p, int64_t i, int type) {
     return (float)static_cast<const __bf16 *>(p)[i];
 }
 
-// x / (1 + exp(-x)).
-__device__ __forceinline__ float silu(float x) { return x / (1.0f + expf(-x)); }
+// x / (1 + exp(-x)) within 7 steps of 2^-24: the exponential of -|x|, which
+// does not overflow, from the hardware's exponential of 2, the product with
+// log2 e carried in two parts, and the hardware's reciprocal, refined once.
+// The library's exponential and a division took 60 us of the 354 that a gated
+// product of 32768 x 4096 x 2816 took.
+__device__ __forceinline__ float silu(float x) {
+    const float a = fminf(fabsf(x), 200.0f);        // from there on the result is 0, or x; NaN comes back with x
+    const float t = a * -1.44269502f;               // log2 e, cut
+    const float rest = fmaf(a, -1.44269502f, -t) - a * 1.92596303e-8f;
+    const bool tiny = t < -100.0f;                  // below the normal numbers at -126: two factors
+    float e = __builtin_amdgcn_exp2f(tiny ? t + 64.0f : t);
+    e = fmaf(e, rest * 0.693147182f, e);
+    const float d = 1.0f + (tiny ? 0.0f : e);
+    float r = __builtin_amdgcn_rcpf(d);
+    r = fmaf(r, fmaf(-d, r, 1.0f), r);
+    const float y = x * (x < 0.0f ? e * r : r);
+    return tiny && x < 0.0f ? y * 5.42101086e-20f : y;   // 2^-64
+}
 
 }  // namespace bqm

@@ -92,7 +92,7 @@ int64_t bqm_group_rows_workspace(int count, int groups);
  *             f32 result is rounded once.
  *   rows, slots, n >= 1, slots a multiple of rows, 1 <= groups <=
  *   BQM_MAX_GROUPS, k >= 32, n even with glu (else BQM_EINVAL); k % 32 == 0;
- *   w and xq 16-byte aligned (else BQM_EUNSUPPORTED).
+ *   w and xq 16-byte aligned; xq less than 4 GiB (else BQM_EUNSUPPORTED).
  * Scales as in bqm_mxfp4_gemm.  The order of the sums depends on the sizes, on
  * none of the rows: a slot's result does not depend on the other slots.
  */

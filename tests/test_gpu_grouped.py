@@ -78,6 +78,8 @@ SHAPES = [  # rows, top, groups, k, n
     (1, 1, 1, 32, 2), (1, 2, 4, 64, 34), (3, 2, 5, 96, 66), (16, 4, 8, 288, 130), (40, 2, 3, 1024, 64),
     (65, 3, 4, 1056, 258), (7, 8, 64, 2048, 96), (200, 1, 3, 512, 514), (333, 2, 2, 1440, 320), (130, 6, 100, 544, 190),
     (20, 1, 1024, 256, 36), (500, 4, 1, 128, 70), (64, 8, 16, 4128, 128), (300, 4, 16, 800, 1030),
+    # more tiles of 128 x 128 than a card takes at once: the large tile
+    (300, 2, 64, 544, 2080), (1500, 1, 5, 800, 5150), (700, 2, 3, 288, 6002), (90, 1, 90, 1056, 1602),
 ]
 
 
@@ -106,10 +108,26 @@ def test_grouped_gemm_distributions(bqm, kind, glu):
     check_gemm(bqm, w, ws, xq, xs, rng.permutation(ids), glu)
 
 
-@pytest.mark.parametrize("rows,top,groups", [(24, 4, 8), (400, 2, 4), (1500, 2, 3)])
-def test_grouped_gemm_a_slots_bits_do_not_depend_on_the_others(bqm, rows, top, groups):
+@pytest.mark.parametrize("n", [1, 33, 255, 4098])
+@pytest.mark.parametrize("glu", [False, True])
+def test_grouped_gemm_every_count_of_rows(bqm, n, glu):
+    """Groups of 1, 31, 32, 33 .. 300 rows, of every type, in the small tile and (the widest n) in the large one."""
+    if glu:
+        n *= 2
+    rng = np.random.default_rng(n)
+    counts = [1, 31, 32, 33, 63, 64, 65, 127, 128, 129, 191, 192, 193, 255, 256, 257, 300, 0, 2]
+    ids = rng.permutation(np.repeat(np.arange(len(counts)), counts))
+    k = 96
+    w, ws = random_mx((len(counts), n), k, rng, 122, 126)
+    xq, xs = random_mx((len(ids),), k, rng, 122, 126)
+    for t in TYPES:
+        check_gemm(bqm, w, ws, xq, xs, ids, glu, t)
+
+
+@pytest.mark.parametrize("rows,top,groups,n", [(24, 4, 8, 200), (400, 2, 4, 200), (1500, 2, 3, 200), (1500, 2, 3, 2600)])
+def test_grouped_gemm_a_slots_bits_do_not_depend_on_the_others(bqm, rows, top, groups, n):
     rng = np.random.default_rng(8)
-    k, n = 1056, 200
+    k = 1056
     w, ws = random_mx((groups, n), k, rng, 100, 150)
     xq, xs = random_mx((rows,), k, rng, 100, 150)
     ids = rng.integers(0, groups, rows * top)

@@ -87,7 +87,9 @@ def test_grouped_gemm_validation(L, glu):
     assert f(groups=0) == 1 and f(groups=1025) == 1 and f(k=16) == 1 and f(n=0) == 1
     assert f(k=48) == 2 and f(w=MIS8) == 2 and f(xq=MIS8) == 2
     assert f(off=MIS2) == 2 and f(order=MIS2) == 2 and f(y=MIS2) == 2 and f(yt=1, y=ODD) == 2
-    assert f(rows=2 ** 30, slots=2 ** 30, n=2 ** 20) == 2    # more tiles than a dispatch counts
+    assert f(rows=2 ** 26, slots=2 ** 30, k=32, n=2 ** 20) == 2    # more tiles than a dispatch counts
+    assert f(rows=2 ** 23, slots=2 ** 23, k=1024) == 2      # x of 4 GiB
+    assert f(k=(1 << 22) + 32) == 2
     if glu:
         assert f(n=7) == 1
 
