@@ -12,10 +12,20 @@
 //    of each half) of one expert for up to T slots.  It finds them itself: a
 //    slot's workgroup looks at all ids, and works if its slot is the first,
 //    or the (T i)-th, of those with its id.
-//  * The slots' rows are cut into LDS once.  The waves share k in slices of
-//    512, or units where a row has few slices; weights stream two tiles of 16
-//    rows ahead and pass through a wave's own LDS tile, and the waves' sums
-//    meet in LDS, added in wave order.
+//  * The slots' rows are cut into LDS once.  A wave goes through a unit's k in
+//    slices of 512 by itself, without a barrier; where there are few units,
+//    several waves share its slices and their sums meet in LDS, added in wave
+//    order.  Weights stream a slice of both tiles ahead and pass through a
+//    wave's own LDS tile, 256 contiguous bytes a row from memory.
+//  * Two workgroups of eight waves a compute unit: one starts (ids, x) while
+//    the other streams.  One a compute unit, with two slices ahead, took 54 us
+//    instead of 35 at 54 slots of 64 experts, 1408 x 4096, and 145 instead of
+//    60 at 48 of 60, 5120 x 3328.
+//
+// Weights from HBM, in a graph: 8 slots of 64 experts, 4096 x 2816 with the
+// gate, 16 us (49 MB: 9.6 at 5.1 TB/s; ids, x and the first weights are three
+// trips to memory that follow each other), 54 slots, 1408 x 4096, 35 us (22.7),
+// 48 of 60, 5120 x 3328 with the gate, 60 us (at the copy's rate).
 #include "groups.h"
 
 namespace bqm {
@@ -29,6 +39,7 @@ constexpr int kEvBlocks = kEvSlice / 32;
 constexpr int kEvTileStride = kEvSlice / 2 + 16;
 constexpr int kEvTileBytes = 16 * kEvTileStride;
 constexpr int kEvSlots = 5;             // of a workgroup, at most
+constexpr int kEvPlace = 32;            // bytes of the list of slots
 constexpr int kEvLds = 160 * 1024;
 
 struct EvArgs {
@@ -73,8 +84,9 @@ __device__ __forceinline__ v8bf ev_eight(unsigned q, float s) {
 
 // WIDE: scale rows are whole, aligned dwords (k % 128 == 0); else bytes.
 template <bool WIDE>
-__global__ __launch_bounds__(kEvWaves * 64, 2) void expert_gemv_kernel(EvArgs a) {
+__global__ __launch_bounds__(kEvWaves * 64, 4) void expert_gemv_kernel(EvArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    int *const place = reinterpret_cast<int *>(lds);   // the slots that this workgroup takes
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, g4 = lane >> 4;
@@ -86,41 +98,43 @@ __global__ __launch_bounds__(kEvWaves * 64, 2) void expert_gemv_kernel(EvArgs a)
     if (unit0 >= unit1) return;
 
     // the slots with this slot's expert
-    const int expert = a.ids[slot0];
+    int all[BQM_EXPERT_GEMV_MAX_SLOTS / 64], expert = 0;
+#pragma unroll
+    for (int j = 0; j < BQM_EXPERT_GEMV_MAX_SLOTS / 64; j++) all[j] = 64 * j < a.slots ? a.ids[min(64 * j + lane, a.slots - 1)] : 0;
+#pragma unroll
+    for (int j = 0; j < BQM_EXPERT_GEMV_MAX_SLOTS / 64; j++)
+        if (slot0 >> 6 == j) expert = __builtin_amdgcn_readlane(all[j], slot0 & 63);
     if ((unsigned)expert >= (unsigned)a.groups) {
         const int lo = unit0 * per_unit, hi = min(unit1 * per_unit, outs);
-        for (int i = lo + tid; i < hi; i += kEvWaves * 64) a.y[(int64_t)slot0 * outs + i] = 0.0f;
+        for (int i = lo + tid; i < hi; i += blockDim.x) a.y[(int64_t)slot0 * outs + i] = 0.0f;
         return;
     }
-    int mine[kEvSlots], count = 0, before = 0;
-#pragma unroll
-    for (int i = 0; i < kEvSlots; i++) mine[i] = slot0;
+    int count = 0, before = 0;
 #pragma unroll
     for (int j = 0; j < BQM_EXPERT_GEMV_MAX_SLOTS / 64; j++) {
         const int s = 64 * j + lane;
-        uint64_t same = __ballot(s < a.slots && a.ids[min(s, a.slots - 1)] == expert);
+        uint64_t same = __ballot(s < a.slots && all[j] == expert);
         const int up = slot0 - 64 * j;   // lanes below it are earlier slots
         const uint64_t earlier = up <= 0 ? 0 : up >= 64 ? ~(uint64_t)0 : ((uint64_t)1 << up) - 1;
         before += __builtin_popcountll(same & earlier);
         same &= ~earlier;
         while (same != 0 && count < a.take) {
-            const int at = 64 * j + __builtin_ctzll(same);
-#pragma unroll
-            for (int i = 0; i < kEvSlots; i++)
-                if (i == count) mine[i] = at;
+            if (tid == 0) place[count] = 64 * j + __builtin_ctzll(same);
             count++;
             same &= same - 1;
         }
     }
     if (before % a.take != 0) return;
+    __syncthreads();
 
     const int nblk = a.k / 32;
     const int64_t row_bytes = a.k / 2;
     const int xstride = a.slices * kEvSlice * 2 + 16;
-    uint8_t *const xs = lds;
-    uint8_t *const tile = lds + 3 * a.take * xstride + wave * kEvTileBytes;
-    float2 *const red = reinterpret_cast<float2 *>(lds + 3 * a.take * xstride + kEvWaves * kEvTileBytes);   // [2][waves][2][64]
-    const int sub = wave / a.parts, wpart = wave % a.parts;   // sub == subs: a wave without work
+    const int waves = a.parts * a.subs;
+    uint8_t *const xs = lds + kEvPlace;
+    uint8_t *const tile = xs + 3 * a.take * xstride + wave * kEvTileBytes;
+    float2 *const red = reinterpret_cast<float2 *>(xs + 3 * a.take * xstride + waves * kEvTileBytes);   // [2][waves][2][64]
+    const int sub = wave / a.parts, wpart = wave % a.parts;
     const uint8_t *const w = a.w + (int64_t)expert * a.n * row_bytes;
     const uint8_t *const ws = a.ws + (int64_t)expert * a.n * nblk;
 
@@ -136,7 +150,7 @@ __global__ __launch_bounds__(kEvWaves * 64, 2) void expert_gemv_kernel(EvArgs a)
         for (int h = 0; h < 2; h++) {
             const int j0 = next_unit * per_unit + (a.glu ? 0 : 16 * h);
             const int64_t row0 = j0 + (a.glu ? (int64_t)h * outs : 0);
-            const int rows = next_unit < unit1 && sub < a.subs ? min(outs - j0, 16) : 0;   // may be <= 0: nothing is read
+            const int rows = next_unit < unit1 ? min(outs - j0, 16) : 0;   // may be <= 0: nothing is read
             const __amdgpu_buffer_rsrc_t rw = mx_rsrc(w + row0 * row_bytes, rows * row_bytes);
             const __amdgpu_buffer_rsrc_t rs = mx_rsrc(ws + row0 * nblk, (int64_t)rows * nblk);
             const uint32_t off = blk0 + r16 < nblk ? (uint32_t)(g4 * row_bytes + 16 * (blk0 + r16)) : 0x80000000u;
@@ -159,15 +173,14 @@ __global__ __launch_bounds__(kEvWaves * 64, 2) void expert_gemv_kernel(EvArgs a)
             next_unit += a.subs;
         }
     };
-    Tile it[2][2];
-    load(it[0]);
+    Tile it[2];
+    load(it);
 
     // the slots' rows, eight values a thread and turn; zeros up to a whole slice
     const int per_row = a.slices * 64;
-    for (int i = 0; i < kEvSlots; i++) {
-        if (i >= count) break;
-        const float *const x = a.x + (int64_t)(mine[i] / a.top) * a.k;
-        for (int at = tid; at < per_row; at += kEvWaves * 64) {
+    for (int i = 0; i < count; i++) {
+        const float *const x = a.x + (int64_t)(__builtin_amdgcn_readfirstlane(place[i]) / a.top) * a.k;
+        for (int at = tid; at < per_row; at += blockDim.x) {
             u32x4 v[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}}, p[3];
             if (8 * at < a.k) {
                 v[0] = *reinterpret_cast<const u32x4 *>(x + 8 * at);
@@ -178,7 +191,6 @@ __global__ __launch_bounds__(kEvWaves * 64, 2) void expert_gemv_kernel(EvArgs a)
             for (int h = 0; h < 3; h++) *reinterpret_cast<u32x4 *>(xs + (3 * i + h) * xstride + 16 * at) = p[h];
         }
     }
-    load(it[1]);
     __syncthreads();
 
     // this lane's operand row: part h of slots 0..3 has rows 4 i + h, of slot 4 rows 4 h + 3
@@ -219,17 +231,49 @@ __global__ __launch_bounds__(kEvWaves * 64, 2) void expert_gemv_kernel(EvArgs a)
             }
         if (++s < a.per_wave) return;
         s = 0;
-        // lane: weight row r16; (its slot's sum, slot 4's part), the smallest part first
-        float2 *const out = red + set * (kEvWaves * 128);
+        // lane: weight row r16; its slot's sum, and a part of slot 4's, the smallest part first
+        float mine_sum[2], fifth[2];
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            out[(wave * 2 + h) * 64 + lane] = make_float2((acc[h][2] + acc[h][1]) + acc[h][0], acc[h][3]);
+            mine_sum[h] = (acc[h][2] + acc[h][1]) + acc[h][0];
+            fifth[h] = acc[h][3];
             acc[h] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
         }
+        if (a.parts == 1) {
+            // the wave has its unit's sums: slot g4 of lanes r16, slot 4 of the first ones
+            const int u = unit + sub;
+            auto put = [&](int tok, float p0, float p1) {
+                float *const to = a.y + (int64_t)place[tok] * outs;
+                const int j = u * per_unit + r16;
+                if (a.glu) {
+                    if (j < outs) to[j] = silu(p0) * p1;
+                } else {
+                    if (j < outs) to[j] = p0;
+                    if (j + 16 < outs) to[j + 16] = p1;
+                }
+            };
+            if (u < unit1) {
+                if (g4 < count) put(g4, mine_sum[0], mine_sum[1]);
+                if (count > 4) {
+                    float p[2];
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const float b = __shfl(fifth[h], r16 + 16), c = __shfl(fifth[h], r16 + 32);
+                        p[h] = (c + b) + fifth[h];
+                    }
+                    if (g4 == 0) put(4, p[0], p[1]);
+                }
+            }
+            unit += a.subs;
+            return;
+        }
+        float2 *const out = red + set * (waves * 128);
+#pragma unroll
+        for (int h = 0; h < 2; h++) out[(wave * 2 + h) * 64 + lane] = make_float2(mine_sum[h], fifth[h]);
         __syncthreads();
         // an output a thread: slot, sub, column (of 32 weight rows, or 16 pairs)
         const int per = per_unit * count;
-        for (int o = tid; o < per * a.subs; o += kEvWaves * 64) {
+        for (int o = tid; o < per * a.subs; o += blockDim.x) {
             const int su = o / per, in = o - su * per, tok = in / per_unit, col = in - tok * per_unit;
             const int j = (unit + su) * per_unit + col;
             if (unit + su >= unit1 || j >= outs) continue;
@@ -242,30 +286,23 @@ __global__ __launch_bounds__(kEvWaves * 64, 2) void expert_gemv_kernel(EvArgs a)
                 }
                 return sum;
             };
-            int at = mine[0];
-#pragma unroll
-            for (int i = 1; i < kEvSlots; i++)
-                if (i == tok) at = mine[i];
             float v;
             if (a.glu)
                 v = silu(total(0, col)) * total(1, col);
             else
                 v = total(col >> 4, col & 15);
-            a.y[(int64_t)at * outs + j] = v;
+            a.y[(int64_t)place[tok] * outs + j] = v;
         }
         unit += a.subs;
         set ^= 1;
     };
-    const int rounds = (unit1 - unit0 + a.subs - 1) / a.subs * a.per_wave;   // the same for all waves
+    const int rounds = (unit1 - unit0 + a.subs - 1) / a.subs * a.per_wave;   // the same for all waves, which meet
 #pragma unroll 1
-    for (int j = 0; j < rounds; j += 2) {
-        item(it[0]);
-        if (j + 1 < rounds) item(it[1]);
-    }
+    for (int j = 0; j < rounds; j++) item(it);
 }
 
-static int64_t ev_lds(int take, int slices) {
-    return 3ll * take * (slices * kEvSlice * 2 + 16) + kEvWaves * kEvTileBytes + 2 * kEvWaves * 128 * (int)sizeof(float2);
+static int64_t ev_lds(int take, int slices, int waves) {
+    return kEvPlace + 3ll * take * (slices * kEvSlice * 2 + 16) + (int64_t)waves * (kEvTileBytes + 2 * 128 * (int)sizeof(float2));
 }
 
 }  // namespace bqm
@@ -285,23 +322,42 @@ extern "C" int bqm_mxfp4_expert_gemv(const uint8_t *w, const uint8_t *ws, const 
     if (rc) return rc;
     EvArgs a = {w, ws, x, ids, y, slots / rows, slots, groups, k, n, glu != 0, 0, 0, 0, 0, 0, 0};
     a.slices = (k + kEvSlice - 1) / kEvSlice;
-    a.parts = a.slices < kEvWaves ? a.slices : kEvWaves;
+    // As many distinct ids as slots choose by chance have work.
+    const int per_unit = glu ? 16 : 32, cus = device_cus();
+    const int units = ((glu ? n / 2 : n) + per_unit - 1) / per_unit;
+    double distinct = slots;
+    if (rows > 1) {
+        double missed = 1.0;
+        for (int i = 0; i < slots; i++) missed *= 1.0 - 1.0 / groups;
+        distinct = groups * (1.0 - missed);
+    }
+    // Waves share k as far as there are fewer units than four a compute unit
+    // (8 slots, 4096 x 2816: 15.6 us with four waves a unit, 22 with one, 17.8
+    // with eight; 4 x 4, 2048 x 1536: 10.5 with four, 12.8 with one).
+    a.parts = 1;
+    while (distinct * units * a.parts < 4.0 * cus && a.parts < kEvWaves && a.parts < a.slices) a.parts *= 2;
+    if (a.parts > a.slices) a.parts = a.slices;
     a.subs = kEvWaves / a.parts;
     a.per_wave = (a.slices + a.parts - 1) / a.parts;
-    a.take = rows == 1 ? 1 : kEvSlots;   // one token's experts are different ones
-    while (a.take > 1 && ev_lds(a.take, a.slices) > kEvLds) a.take--;
-    const int per_unit = glu ? 16 : 32;
-    const int units = ((glu ? n / 2 : n) + per_unit - 1) / per_unit;
-    // as many workgroups as compute units, each with whole rounds of its waves
-    int strips = device_cus() / slots;
-    if (strips < 1) strips = 1;
-    a.each = ((units + strips - 1) / strips + a.subs - 1) / a.subs * a.subs;
+    const int waves = a.parts * a.subs;
+    // Slots of an expert that a workgroup takes: about twice what an expert has
+    // on average, since their operand costs LDS, and a second workgroup finds
+    // the weights in the caches.
+    a.take = rows == 1 ? 1 : 1 + 2 * slots / groups;   // one token's experts are different ones
+    if (a.take > kEvSlots) a.take = kEvSlots;
+    while (a.take > 1 && ev_lds(a.take, a.slices, waves) > kEvLds) a.take--;
+    const int bytes = (int)ev_lds(a.take, a.slices, waves);
+    // Units of a workgroup: one a wave (or group of waves), or as many more as
+    // keep the workgroups that work to two a compute unit.
+    const double most = 2.0 * cus / distinct;   // workgroups of an expert
+    const int strips = most < 1.0 ? 1 : (int)most;
+    const int rounds = (units + a.subs - 1) / a.subs;
+    a.each = (rounds + strips - 1) / strips * a.subs;
     const dim3 grid((unsigned)((units + a.each - 1) / a.each), (unsigned)slots);
-    const int bytes = (int)ev_lds(a.take, a.slices);
     hipStream_t s = as_stream(stream);
     if (wide)
-        hipLaunchKernelGGL(expert_gemv_kernel<true>, grid, dim3(kEvWaves * 64), bytes, s, a);
+        hipLaunchKernelGGL(expert_gemv_kernel<true>, grid, dim3(waves * 64), bytes, s, a);
     else
-        hipLaunchKernelGGL(expert_gemv_kernel<false>, grid, dim3(kEvWaves * 64), bytes, s, a);
+        hipLaunchKernelGGL(expert_gemv_kernel<false>, grid, dim3(waves * 64), bytes, s, a);
     return launch_status();
 }
