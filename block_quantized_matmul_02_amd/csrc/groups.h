@@ -19,6 +19,18 @@ struct GroupTile {
     int first, rows, local;
 };
 
+// Sum over this lane and the ones below it: within a row of 16 lanes by shifts,
+// then the rows before it.
+__device__ __forceinline__ int wave_upto(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast 15 to rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast 31 to rows 2 and 3
+    return v;
+}
+
 // Item `id` of the list in which every group has ceil(rows / bm) * mult items,
 // the rows of no group last.  A wave looks at 64 groups at a time; uniform.
 // Offsets are taken into 0..slots, so positions are always inside order.
@@ -27,16 +39,13 @@ __device__ __forceinline__ GroupTile find_group(const Grouping &q, int bm, int m
     int before = 0;
     for (int base = 0; base <= q.groups; base += 64) {
         const int g = base + lane;
-        const int lo = g <= q.groups ? min(max(q.offsets[g], 0), q.slots) : q.slots;
-        const int hi = g < q.groups ? min(max(q.offsets[g + 1], 0), q.slots) : q.slots;
+        // both at once, without a branch: a group past the last is empty, the last one ends with the slots
+        const int from = q.offsets[min(g, q.groups)], to = q.offsets[min(g + 1, q.groups)];
+        const int lo = g <= q.groups ? min(max(from, 0), q.slots) : q.slots;
+        const int hi = g < q.groups ? min(max(to, 0), q.slots) : q.slots;
         const int rows = max(hi - lo, 0);
         const int items = (rows + bm - 1) / bm * mult;
-        int upto = items;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int other = __shfl_up(upto, d);
-            if (lane >= d) upto += other;
-        }
+        const int upto = wave_upto(items);
         const uint64_t past = __ballot(before + upto > id);
         if (past != 0) {
             const int at = __builtin_ctzll(past);

@@ -173,12 +173,7 @@ __global__ __launch_bounds__(kGrWaves * 64) void group_rows_kernel(GroupRowsArgs
         }
     }
     // where each group begins: exclusive sums over the groups, group 1024 last
-    int upto = mine[0];
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int other = __shfl_up(upto, d);
-        if (lane >= d) upto += other;
-    }
+    const int upto = wave_upto(mine[0]);
     if (lane == 63) wave_total[wave] = upto;
     __syncthreads();
     int before = 0, total = 0;
