@@ -26,6 +26,7 @@ E4M3_GEMV_MAX_M = 16
 MXFP4_GEMV_MAX_M = 16
 LOGPROBS_MAX_TOP = 32
 MAX_GROUPS = 1024
+MAX_ROWS = 16777216
 MAX_TOP = 32
 EXPERT_GEMV_MAX_SLOTS = 256
 EXPERT_GEMV_MAX_K = 16384

@@ -8,25 +8,42 @@
 //  * Choice: a wave a row, its logits in registers (column 64 j + lane); each
 //    turn takes the wave's largest and, of equals, the first register with it
 //    and there the first lane, which is the lowest column.
-//  * Sort by counting: a workgroup counts 4096 rows, each wave its own 256 in
+//    The search is on whole numbers of the values' order.
+//  * Sort by counting: a workgroup counts 2048 rows, each wave its own 256 in
 //    order, so that a row's place is (rows of lower groups) + (rows of its
 //    group in earlier chunks, waves, batches and lanes): no atomics, the same
 //    order every time.  Equal ids of a wave are found by a ballot for each bit
-//    of the id.  More rows take two launches, the chunks' counts in between.
+//    of the id.  More rows take two launches, the chunks' counts in between;
+//    at most 64 take a wave that compares them with each other.
+//
+// In a graph: 1 x 128, 8 of them, and their sort 4.6 us (two launches); 8192 x
+// 256 and the sort of 65536 rows 16.5: 8 (the choice: 25 instructions a turn
+// and wave), 2 and 7 us.
 #include "groups.h"
 
 namespace bqm {
 
-__device__ __forceinline__ float wave_max(float v) {
-    auto step = [&](auto ctrl) {
-        const float o = __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 0xF, 0xF, false));
-        v = fmaxf(v, o);
-    };
-    step(std::integral_constant<int, 0xB1>{});
-    step(std::integral_constant<int, 0x4E>{});
-    step(std::integral_constant<int, 0x141>{});
-    step(std::integral_constant<int, 0x140>{});
-    return swap32_max(swap16_max(v));
+// An f32 (no NaN) as a whole number of the same order, -0 as +0, and back.
+__device__ __forceinline__ int order_of(float v) {
+    const int b = __builtin_bit_cast(int, v + 0.0f);
+    return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float value_of(int k) { return __builtin_bit_cast(float, k ^ ((k >> 31) & 0x7FFFFFFF)); }
+
+constexpr int kOut = (int)0x807FFFFF;   // of -inf: not to be chosen
+
+// The wave's largest, uniform: shifts within rows of 16 lanes, then the rows
+// before, into the last lane.  Whole numbers: a step is one instruction, where
+// floats have theirs made quiet first.
+__device__ __forceinline__ int wave_max(int v) {
+    constexpr int none = (int)0x80000000;
+    v = max(v, __builtin_amdgcn_update_dpp(none, v, 0x111, 0xF, 0xF, false));
+    v = max(v, __builtin_amdgcn_update_dpp(none, v, 0x112, 0xF, 0xF, false));
+    v = max(v, __builtin_amdgcn_update_dpp(none, v, 0x114, 0xF, 0xF, false));
+    v = max(v, __builtin_amdgcn_update_dpp(none, v, 0x118, 0xF, 0xF, false));
+    v = max(v, __builtin_amdgcn_update_dpp(none, v, 0x142, 0xA, 0xF, false));
+    v = max(v, __builtin_amdgcn_update_dpp(none, v, 0x143, 0xC, 0xF, false));
+    return __builtin_amdgcn_readlane(v, 63);
 }
 
 struct RouteArgs {
@@ -34,61 +51,57 @@ struct RouteArgs {
     int64_t ld;
     int *ids;
     float *weights;
-    int type, top, renorm, m, e;
+    int top, renorm, m, e;
 };
 
 // J: registers of a lane, 64 J >= e.
-template <int J>
+template <typename T, int J>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     const int lane = threadIdx.x & 63;
     const int64_t t = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (t >= a.m) return;
+    // all loads at once, without branches: past the end the last column again
+    const T *const logits = static_cast<const T *>(a.logits) + t * a.ld;
     float v[J];
+    int key[J];
     bool bad = false;
 #pragma unroll
+    for (int j = 0; j < J; j++) v[j] = (float)logits[min(64 * j + lane, a.e - 1)];
+#pragma unroll
     for (int j = 0; j < J; j++) {
-        const int c = 64 * j + lane;
-        v[j] = c < a.e ? load_as(a.logits, t * a.ld + c, a.type) : -INFINITY;
         bad |= !(v[j] < INFINITY);   // NaN or +inf
-        if (v[j] != v[j]) v[j] = -INFINITY;
+        key[j] = v[j] != v[j] || 64 * j + lane >= a.e ? kOut : order_of(v[j]);
     }
     const bool poison = __ballot(bad) != 0;
-    float most = v[0];
-#pragma unroll
-    for (int j = 1; j < J; j++) most = fmaxf(most, v[j]);
-    most = wave_max(most);
-    float z = 0.0f;
-    if (!a.renorm && most > -INFINITY) {
-#pragma unroll
-        for (int j = 0; j < J; j++) z += expf(v[j] - most);
-        z = wave_sum(z);
-    }
     // lane i keeps choice i
-    int id = -1;
-    float value = -INFINITY;
+    int id = -1, chosen = kOut, most = kOut;
     for (int i = 0; i < a.top; i++) {
-        float here = v[0];
+        int here = key[0];
 #pragma unroll
-        for (int j = 1; j < J; j++) here = fmaxf(here, v[j]);
+        for (int j = 1; j < J; j++) here = max(here, key[j]);
         here = wave_max(here);
-        if (here == -INFINITY) break;
-        bool found = false;
+        if (here == kOut) break;
+        if (i == 0) most = here;
+        // of equals the first register, and there the first lane
+        int at = -1;
 #pragma unroll
-        for (int j = 0; j < J; j++) {
-            const uint64_t equal = __ballot(v[j] == here);
-            if (!found && equal != 0) {
-                found = true;
-                const int at = __builtin_ctzll(equal);
-                if (lane == at) v[j] = -INFINITY;
-                if (lane == i) {
-                    id = 64 * j + at;
-                    value = here;
-                }
-            }
+        for (int j = J - 1; j >= 0; j--) {
+            const uint64_t equal = __ballot(key[j] == here);
+            at = equal != 0 ? 64 * j + __builtin_ctzll(equal) : at;
         }
+#pragma unroll
+        for (int j = 0; j < J; j++) key[j] = 64 * j + lane == at ? kOut : key[j];
+        id = lane == i ? at : id;
+        chosen = lane == i ? here : chosen;
     }
-    float w = id >= 0 ? expf(value - most) : 0.0f;
-    if (a.renorm) z = wave_sum(w);
+    const float top = value_of(most);
+    float w = id >= 0 ? expf(value_of(chosen) - top) : 0.0f, z = w;
+    if (!a.renorm && most != kOut) {
+        z = 0.0f;
+#pragma unroll
+        for (int j = 0; j < J; j++) z += v[j] == v[j] && 64 * j + lane < a.e ? expf(v[j] - top) : 0.0f;
+    }
+    z = wave_sum(z);
     if (id >= 0) w = poison ? NAN : w / z;
     if (lane < a.top) {
         a.ids[t * a.top + lane] = id;
@@ -96,9 +109,26 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     }
 }
 
-constexpr int kGrWaves = 16;
+template <typename T>
+static int launch_route(const RouteArgs &a, unsigned grid, hipStream_t s) {
+    const dim3 g(grid), b(256);
+    if (a.e <= 64)
+        hipLaunchKernelGGL((route_kernel<T, 1>), g, b, 0, s, a);
+    else if (a.e <= 128)
+        hipLaunchKernelGGL((route_kernel<T, 2>), g, b, 0, s, a);
+    else if (a.e <= 256)
+        hipLaunchKernelGGL((route_kernel<T, 4>), g, b, 0, s, a);
+    else if (a.e <= 512)
+        hipLaunchKernelGGL((route_kernel<T, 8>), g, b, 0, s, a);
+    else
+        hipLaunchKernelGGL((route_kernel<T, 16>), g, b, 0, s, a);
+    return launch_status();
+}
+
+constexpr int kGrWaves = 8;
+constexpr int kGrThreads = kGrWaves * 64;
 constexpr int kGrBatches = 4;                               // of 64 rows, a wave
-constexpr int kGrChunk = kGrWaves * kGrBatches * 64;        // rows of a workgroup
+constexpr int kGrChunk = kGrThreads * kGrBatches;        // rows of a workgroup
 
 struct GroupRowsArgs {
     const int *ids;
@@ -106,11 +136,31 @@ struct GroupRowsArgs {
     int count, groups, chunks, bits;
 };
 
-// MODE 0: all rows in one workgroup.  1: a chunk's counts.  2: a chunk's places.
-template <int MODE>
-__global__ __launch_bounds__(kGrWaves * 64) void group_rows_kernel(GroupRowsArgs a) {
+// A chunk's counts.  Whole numbers: the order in which they are added is free.
+__global__ __launch_bounds__(kGrThreads) void group_count_kernel(GroupRowsArgs a) {
+    __shared__ int hist[BQM_MAX_GROUPS + 1];
+    const int tid = threadIdx.x, all = a.groups + 1;
+    const int64_t row0 = (int64_t)blockIdx.x * kGrChunk + tid;
+    int id[kGrBatches];
+#pragma unroll
+    for (int b = 0; b < kGrBatches; b++) {
+        const int64_t row = row0 + b * (kGrThreads);
+        id[b] = a.ids[row < a.count ? row : a.count - 1];
+    }
+    for (int i = tid; i < all; i += kGrThreads) hist[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < kGrBatches; b++)
+        if (row0 + b * (kGrThreads) < a.count) atomicAdd(&hist[(unsigned)id[b] < (unsigned)a.groups ? id[b] : a.groups], 1);
+    __syncthreads();
+    for (int i = tid; i < all; i += kGrThreads) a.counts[(int64_t)blockIdx.x * all + i] = hist[i];
+}
+
+// CHUNKS: more than one workgroup, whose counts are known.
+template <bool CHUNKS>
+__global__ __launch_bounds__(kGrThreads) void group_rows_kernel(GroupRowsArgs a) {
     extern __shared__ int lds[];
-    __shared__ int wave_total[kGrWaves];
+    __shared__ int wave_total[BQM_MAX_GROUPS / kGrThreads + 1][kGrWaves];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int all = a.groups + 1;                 // the last one: rows of no group
@@ -123,11 +173,14 @@ __global__ __launch_bounds__(kGrWaves * 64) void group_rows_kernel(GroupRowsArgs
 #pragma unroll
     for (int b = 0; b < kGrBatches; b++) {
         const int64_t row = row0 + 64 * b;
-        id[b] = row < a.count ? a.ids[row] : -1;
-        if ((unsigned)id[b] >= (unsigned)a.groups) id[b] = a.groups;
-        if (row >= a.count) id[b] = -1;
+        id[b] = a.ids[row < a.count ? row : a.count - 1];
     }
-    for (int i = tid; i < kGrWaves * all; i += kGrWaves * 64) lds[i] = 0;
+#pragma unroll
+    for (int b = 0; b < kGrBatches; b++) {
+        if ((unsigned)id[b] >= (unsigned)a.groups) id[b] = a.groups;
+        if (row0 + 64 * b >= a.count) id[b] = -1;
+    }
+    for (int i = tid; i < kGrWaves * all; i += kGrThreads) lds[i] = 0;
     __syncthreads();
 #pragma unroll
     for (int b = 0; b < kGrBatches; b++) {
@@ -142,53 +195,64 @@ __global__ __launch_bounds__(kGrWaves * 64) void group_rows_kernel(GroupRowsArgs
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
     __syncthreads();
-    // per group: the earlier waves' rows, and the chunk's
-    int mine[2] = {0, 0};   // of groups tid and tid + 1024
+    // per group: the earlier waves' rows, the chunk's, the earlier chunks' and all
+    constexpr int H = BQM_MAX_GROUPS / kGrThreads + 1;   // groups of a thread: tid + kGrThreads h
+    int mine[H] = {}, earlier[H] = {};
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
-        const int g = tid + 1024 * h;
+    for (int h = 0; h < H; h++) {
+        const int g = tid + kGrThreads * h;
         if (g >= all) continue;
-        int sum = 0;
+        int c[kGrWaves], sum = 0;
+#pragma unroll
+        for (int w = 0; w < kGrWaves; w++) c[w] = lds[w * all + g];
+#pragma unroll
         for (int w = 0; w < kGrWaves; w++) {
-            const int c = lds[w * all + g];
             lds[w * all + g] = sum;
-            sum += c;
+            sum += c[w];
         }
         mine[h] = sum;
-        if (MODE == 1) a.counts[(int64_t)blockIdx.x * all + g] = sum;
     }
-    if (MODE == 1) return;
-    int earlier[2] = {0, 0};
-    if (MODE == 2) {
+    if (CHUNKS) {
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const int g = tid + 1024 * h;
+        for (int h = 0; h < H; h++) {
+            const int g = tid + kGrThreads * h;
             if (g >= all) continue;
-            int sum = 0;
-            for (int c = 0; c < a.chunks; c++) {
-                if (c == (int)blockIdx.x) earlier[h] = sum;
-                sum += a.counts[(int64_t)c * all + g];
+            int sum = 0, before = 0;
+            for (int c0 = 0; c0 < a.chunks; c0 += 32) {
+                int c[32];   // all on their way together
+#pragma unroll
+                for (int i = 0; i < 32; i++) c[i] = a.counts[(int64_t)min(c0 + i, a.chunks - 1) * all + g];
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int i = 0; i < 32; i++) {
+                    before += c0 + i < (int)blockIdx.x ? c[i] : 0;
+                    sum += c0 + i < a.chunks ? c[i] : 0;
+                }
             }
+            earlier[h] = before;
             mine[h] = sum;
         }
     }
-    // where each group begins: exclusive sums over the groups, group 1024 last
-    const int upto = wave_upto(mine[0]);
-    if (lane == 63) wave_total[wave] = upto;
-    __syncthreads();
-    int before = 0, total = 0;
-    for (int w = 0; w < kGrWaves; w++) {
-        if (w < wave) before += wave_total[w];
-        total += wave_total[w];
-    }
-    const int begin = before + upto - mine[0];
-    if (tid < all) {
-        base[tid] = begin + earlier[0];
-        if (blockIdx.x == 0) a.offsets[tid] = begin;
-    }
-    if (tid + 1024 < all) {
-        base[tid + 1024] = total + earlier[1];
-        if (blockIdx.x == 0) a.offsets[tid + 1024] = total;
+    // where each group begins: exclusive sums over the groups
+    int done = 0;
+#pragma unroll
+    for (int h = 0; h < H; h++) {
+        if (kGrThreads * h >= all) break;
+        const int upto = wave_upto(mine[h]);
+        if (lane == 63) wave_total[h][wave] = upto;
+        __syncthreads();
+        int before = done;
+#pragma unroll
+        for (int w = 0; w < kGrWaves; w++) {
+            const int c = wave_total[h][w];
+            before += w < wave ? c : 0;
+            done += c;
+        }
+        const int g = tid + kGrThreads * h, begin = before + upto - mine[h];
+        if (g < all) {
+            base[g] = begin + earlier[h];
+            if (blockIdx.x == 0) a.offsets[g] = begin;
+        }
     }
     __syncthreads();
 #pragma unroll
@@ -204,13 +268,33 @@ __global__ __launch_bounds__(kGrWaves * 64) void group_rows_kernel(GroupRowsArgs
     }
 }
 
-template <int MODE>
+// At most 64 rows and 256 groups: one wave without LDS.  A row's place is the
+// rows of lower groups and the earlier ones of its own.
+__global__ __launch_bounds__(64) void group_few_kernel(GroupRowsArgs a) {
+    constexpr int I = 5;   // groups of a lane: lane, lane + 64, ..
+    const int lane = threadIdx.x;
+    int id = a.ids[min(lane, a.count - 1)];
+    if ((unsigned)id >= (unsigned)a.groups) id = a.groups;
+    int place = 0, begin[I] = {};
+    for (int j = 0; j < a.count; j++) {
+        const int other = __builtin_amdgcn_readlane(id, j);
+        place += other < id || (other == id && j < lane) ? 1 : 0;
+#pragma unroll
+        for (int i = 0; i < I; i++) begin[i] += other < 64 * i + lane ? 1 : 0;
+    }
+    if (lane < a.count) a.order[place] = lane;
+#pragma unroll
+    for (int i = 0; i < I; i++)
+        if (64 * i + lane <= a.groups) a.offsets[64 * i + lane] = begin[i];
+}
+
+template <bool CHUNKS>
 static int launch_group_rows(const GroupRowsArgs &a, hipStream_t s) {
     static LaunchCache cache;
     const int bytes = (kGrWaves + 1) * (a.groups + 1) * 4;
-    const int rc = raise_lds_limit(cache, reinterpret_cast<const void *>(&group_rows_kernel<MODE>), (kGrWaves + 1) * (BQM_MAX_GROUPS + 1) * 4);
+    const int rc = raise_lds_limit(cache, reinterpret_cast<const void *>(&group_rows_kernel<CHUNKS>), (kGrWaves + 1) * (BQM_MAX_GROUPS + 1) * 4);
     if (rc) return rc;
-    hipLaunchKernelGGL(group_rows_kernel<MODE>, dim3(a.chunks), dim3(kGrWaves * 64), bytes, s, a);
+    hipLaunchKernelGGL(group_rows_kernel<CHUNKS>, dim3(a.chunks), dim3(kGrThreads), bytes, s, a);
     return launch_status();
 }
 
@@ -224,25 +308,15 @@ extern "C" int bqm_route(const void *logits, int64_t ld, int type, int top, int 
     if ((m > 1 && ld < e) || !aligned(logits, type_bytes(type)) || !aligned(ids, 4) || !aligned(weights, 4)) return BQM_EUNSUPPORTED;
     const int64_t grid = ((int64_t)m + 3) / 4;
     if (grid * 256 > 0x7FFFFFFFll) return BQM_EUNSUPPORTED;   // work items that a dispatch counts
-    const RouteArgs a = {logits, m > 1 ? ld : 0, ids, weights, type, top, renorm, m, e};
+    const RouteArgs a = {logits, m > 1 ? ld : 0, ids, weights, top, renorm, m, e};
     hipStream_t s = as_stream(stream);
-    const dim3 g((unsigned)grid), b(256);
-    if (e <= 64)
-        hipLaunchKernelGGL(route_kernel<1>, g, b, 0, s, a);
-    else if (e <= 128)
-        hipLaunchKernelGGL(route_kernel<2>, g, b, 0, s, a);
-    else if (e <= 256)
-        hipLaunchKernelGGL(route_kernel<4>, g, b, 0, s, a);
-    else if (e <= 512)
-        hipLaunchKernelGGL(route_kernel<8>, g, b, 0, s, a);
-    else
-        hipLaunchKernelGGL(route_kernel<16>, g, b, 0, s, a);
-    return launch_status();
+    if (type == BQM_F32) return launch_route<float>(a, (unsigned)grid, s);
+    return type == BQM_F16 ? launch_route<_Float16>(a, (unsigned)grid, s) : launch_route<__bf16>(a, (unsigned)grid, s);
 }
 
 extern "C" int64_t bqm_group_rows_workspace(int count, int groups) {
     using namespace bqm;
-    if (count < 1 || count > 1 << 30 || groups < 1 || groups > BQM_MAX_GROUPS) return -1;
+    if (count < 1 || count > BQM_MAX_ROWS || groups < 1 || groups > BQM_MAX_GROUPS) return -1;
     const int64_t chunks = ((int64_t)count + kGrChunk - 1) / kGrChunk;
     return chunks == 1 ? 0 : chunks * (groups + 1) * 4;
 }
@@ -257,7 +331,12 @@ extern "C" int bqm_group_rows(const int *ids, int count, int groups, int *offset
     GroupRowsArgs a = {ids, offsets, order, static_cast<int *>(workspace), count, groups, (count + kGrChunk - 1) / kGrChunk, 0};
     for (a.bits = 1; (groups >> a.bits) != 0;) a.bits++;   // ids 0..groups
     hipStream_t s = as_stream(stream);
-    if (a.chunks == 1) return launch_group_rows<0>(a, s);
-    const int rc = launch_group_rows<1>(a, s);
-    return rc ? rc : launch_group_rows<2>(a, s);
+    if (count <= 64 && groups <= 256) {
+        hipLaunchKernelGGL(group_few_kernel, dim3(1), dim3(64), 0, s, a);
+        return launch_status();
+    }
+    if (a.chunks == 1) return launch_group_rows<false>(a, s);
+    hipLaunchKernelGGL(group_count_kernel, dim3(a.chunks), dim3(kGrThreads), 0, s, a);
+    const int rc = launch_status();
+    return rc ? rc : launch_group_rows<true>(a, s);
 }

@@ -31,6 +31,8 @@ extern "C" {
 
 /* Largest number of groups (experts, adapters). */
 #define BQM_MAX_GROUPS 1024
+/* Largest count of bqm_group_rows. */
+#define BQM_MAX_ROWS 16777216
 /* Largest top of bqm_route and bqm_combine. */
 #define BQM_MAX_TOP 32
 /* Largest slots and k of bqm_mxfp4_expert_gemv. */
@@ -69,7 +71,8 @@ int bqm_route(const void *logits, int64_t ld, int type, int top, int renorm, int
  *   offsets   : int32 [groups + 1] out;  order : int32 [count] out.
  *   workspace : bqm_group_rows_workspace(count, groups) bytes, 4-byte aligned;
  *               needs no initial contents; NULL if that is 0.
- *   1 <= count <= 2^30, 1 <= groups <= BQM_MAX_GROUPS (else BQM_EINVAL).
+ *   1 <= count <= BQM_MAX_ROWS, 1 <= groups <= BQM_MAX_GROUPS (else
+ *   BQM_EINVAL).
  */
 int bqm_group_rows(const int *ids, int count, int groups, int *offsets, int *order, void *workspace, void *stream);
 
@@ -120,7 +123,7 @@ int bqm_mxfp4_expert_gemv(const uint8_t *w, const uint8_t *ws, const float *x, c
 /*
  * out[t][i] = (res[t][i] +) sum_j weights[t][j] * y[t * top + j][i], j from 0
  * up, in f32, rounded once; the residual is added last.  A slot whose weight
- * is 0 is not read.
+ * is 0 adds nothing, whatever it holds.
  *
  *   y       : y_type [m * top][n], dense.
  *   weights : f32 [m][top].

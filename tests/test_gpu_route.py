@@ -125,6 +125,18 @@ def test_group_rows_many(bqm):
     check_groups(bqm, ids, 128)
 
 
+def test_group_rows_the_most(bqm):
+    rng = np.random.default_rng(4)
+    check_groups(bqm, rng.integers(-1, 1025, bqm.MAX_ROWS).astype(np.int16), 1024)
+
+
+@pytest.mark.parametrize("count", [1, 7, 63, 64, 65])
+@pytest.mark.parametrize("groups", [1, 63, 64, 65, 255, 256, 257])
+def test_group_rows_few(bqm, count, groups):
+    for seed in range(3):
+        check_groups(bqm, np.random.default_rng(seed).integers(-1, groups + 1, count), groups)
+
+
 def combine_ref(y, w, res, m, top):
     v = y.cpu().double().numpy().reshape(m, top, -1)
     c = w.cpu().double().numpy()[:, :, None]

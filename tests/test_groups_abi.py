@@ -48,7 +48,7 @@ def test_constants_match_the_header():
     import block_quantized_matmul_02_amd as bqm
 
     text = open(HEADER).read()
-    for name in ("MAX_GROUPS", "MAX_TOP", "EXPERT_GEMV_MAX_SLOTS", "EXPERT_GEMV_MAX_K", "LORA_MAX_RANK"):
+    for name in ("MAX_GROUPS", "MAX_ROWS", "MAX_TOP", "EXPERT_GEMV_MAX_SLOTS", "EXPERT_GEMV_MAX_K", "LORA_MAX_RANK"):
         assert int(re.search(rf"#define BQM_{name} (\d+)", text).group(1)) == getattr(bqm, name), name
 
 
@@ -68,12 +68,12 @@ def test_group_rows_validation(L):
         return L.bqm_group_rows(ids, count, groups, off, order, ws, NUL)
 
     assert f(ids=NUL) == 1 and f(off=NUL) == 1 and f(order=NUL) == 1
-    assert f(count=0) == 1 and f(count=(1 << 30) + 1) == 1 and f(groups=0) == 1 and f(groups=1025) == 1
+    assert f(count=0) == 1 and f(count=(1 << 24) + 1) == 1 and f(groups=0) == 1 and f(groups=1025) == 1
     assert f(count=100000) == 1                              # needs a workspace
     assert f(ids=MIS2) == 2 and f(off=MIS2) == 2 and f(order=MIS2) == 2 and f(count=100000, ws=MIS2) == 2
     size = L.bqm_group_rows_workspace
-    assert size(0, 4) == -1 and size(10, 0) == -1 and size(10, 1025) == -1 and size((1 << 30) + 1, 4) == -1
-    assert size(1, 1) == 0 and size(64, 1024) == 0 and size(100000, 256) > 0 and size(1 << 30, 1024) > 0
+    assert size(0, 4) == -1 and size(10, 0) == -1 and size(10, 1025) == -1 and size((1 << 24) + 1, 4) == -1
+    assert size(1, 1) == 0 and size(64, 1024) == 0 and size(100000, 256) > 0 and size(1 << 24, 1024) > 0
 
 
 @pytest.mark.parametrize("glu", [0, 1])
