@@ -214,7 +214,7 @@ constexpr int kExpandStrip = kExpandWaves * kExpandTiles * 16;
 
 // S: steps of 32 ranks; G: groups of 16 rows, which share an adapter's operand.
 template <int S, int G, bool F16>
-__global__ __launch_bounds__(kExpandWaves * 64, 4) void lora_expand_kernel(LoraArgs a) {
+__global__ __launch_bounds__(kExpandWaves * 64, S == 8 ? 2 : 4) void lora_expand_kernel(LoraArgs a) {
     __shared__ u32x4 hp[G * S][3][64];   // the parts of h, as the matrix cores take them
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
