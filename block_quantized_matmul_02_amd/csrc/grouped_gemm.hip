@@ -93,7 +93,8 @@ __device__ __forceinline__ int xcd_item(int id, int count) {
 
 // A wave's results to their slots: lane holds column r32 and rows 8 (v / 4) +
 // 4 g + v % 4 of each 32 x 32.  Of 16-bit values two lanes swap, so that each
-// has two columns of one of two rows: half as many stores.
+// has two columns of one of two rows: half as many stores.  Past the caches,
+// where the operands keep their room (7996 slots, 1440 x 5120: 78 us for 94).
 template <typename T, int WM, int TM, int TN, bool GLU>
 __device__ __forceinline__ void store_tile(T *y, int outs, const v16f (&acc)[TM][TN], int te, const int *slots, int j0) {
     const int lane = threadIdx.x & 63, r32 = lane & 31, g = lane >> 5;
@@ -112,7 +113,7 @@ __device__ __forceinline__ void store_tile(T *y, int outs, const v16f (&acc)[TM]
                 if constexpr (sizeof(T) == 4) {
 #pragma unroll
                     for (int e = 0; e < 4; e++)
-                        if (s[e] >= 0 && j < outs) y[(int64_t)s[e] * outs + j] = out[e];
+                        if (s[e] >= 0 && j < outs) __builtin_nontemporal_store(out[e], y + (int64_t)s[e] * outs + j);
                 } else {
                     // even lanes: columns j, j + 1 of row e; odd ones: j - 1, j of row e + 1
                     const bool odd = lane & 1;
@@ -126,7 +127,7 @@ __device__ __forceinline__ void store_tile(T *y, int outs, const v16f (&acc)[TM]
                         if (slot < 0) continue;
                         if (outs % 2 == 0) {   // rows are aligned to two values, and no pair crosses their end
                             typedef T T2 __attribute__((ext_vector_type(2), aligned(2)));
-                            if (col < outs) *reinterpret_cast<T2 *>(to) = T2{lo, hi};
+                            if (col < outs) __builtin_nontemporal_store(T2{lo, hi}, reinterpret_cast<T2 *>(to));
                         } else {
                             if (col < outs) to[0] = lo;
                             if (col + 1 < outs) to[1] = hi;
@@ -165,22 +166,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grouped_gemm_kernel(GgArgs a)
     const int mt = t.local % mtiles, nt = t.local / mtiles;
     const int first = t.first + mt * BM, rows = min(BM, t.rows - mt * BM);
     const int j0 = nt * COLS;
-    for (int i = tid; i < BM; i += NT) {
-        const unsigned s = i < rows ? (unsigned)a.q.order[first + i] : ~0u;
-        slot_of[i] = s < (unsigned)a.q.slots ? (int)s : -1;
-    }
-    __syncthreads();
-    if (t.group == a.q.groups) {   // slots of no group
-        for (int i = tid; i < rows * COLS; i += NT) {
-            const int s = slot_of[i / COLS], j = j0 + i % COLS;
-            if (s >= 0 && j < a.outs) store_as(a.y, (int64_t)s * a.outs + j, 0.0f, a.y_type);
-        }
-        return;
-    }
-
+    const bool none = t.group == a.q.groups;   // slots of no group
     const int64_t rb = a.k / 2;
     const int nblk = a.k / 32;
     const int stages = (nblk + kGgBlocks - 1) / kGgBlocks;
+    // (of no group: nothing is read)
     const uint8_t *const w = a.w + (int64_t)t.group * a.n * rb, *const ws = a.ws + (int64_t)t.group * a.n * nblk;
     const int half = GLU ? a.outs : 0;
 
@@ -189,6 +179,45 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grouped_gemm_kernel(GgArgs a)
     // chunk meet eight different slots
     const int chunk = tid & 7, row = tid >> 3;
     auto slot = [](int r, int c) { return 16 * (c ^ (r & 7)); };
+    // Blocks past the row's end repeat its last one: their scales are 2^-127 on
+    // both sides, whose products vanish in any f32 sum.
+    auto offset = [&](int s) { return 16u * (uint32_t)min(kGgBlocks * s + chunk, nblk - 1); };
+    struct Regs {
+        u32x4 a[CA], b[CB];
+    };
+    Regs R;
+    // the weight rows of a tile follow each other (with the gate those of each
+    // half), so that one offset a thread does for them
+    const int wrows = none ? 0 : min(COLS, a.outs - j0);
+    const __amdgpu_buffer_rsrc_t rB0 = mx_rsrc(w + j0 * rb, wrows * rb);
+    const __amdgpu_buffer_rsrc_t rB1 = mx_rsrc(w + (j0 + half) * rb, wrows * rb);
+    auto load_b = [&](Regs &R, int s) {
+        const uint32_t ob = (uint32_t)((GLU ? row & 31 : row) * rb) + offset(s);
+#pragma unroll
+        for (int i = 0; i < CB; i++) {
+            if constexpr (GLU && RS == 32) {
+                R.b[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(i & 1 ? rB1 : rB0, ob, (i >> 1) * 32 * (int)rb, 0));
+            } else if constexpr (GLU) {
+                R.b[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wave & 4 ? rB1 : rB0, ob, i * 32 * (int)rb, 0));
+            } else {
+                R.b[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rB0, ob, i * RS * (int)rb, 0));
+            }
+        }
+    };
+    // the first weights are on their way while the slots are looked up
+    load_b(R, 0);
+    for (int i = tid; i < BM; i += NT) {
+        const unsigned s = i < rows ? (unsigned)a.q.order[first + i] : ~0u;
+        slot_of[i] = s < (unsigned)a.q.slots ? (int)s : -1;
+    }
+    __syncthreads();
+    if (none) {
+        for (int i = tid; i < rows * COLS; i += NT) {
+            const int s = slot_of[i / COLS], j = j0 + i % COLS;
+            if (s >= 0 && j < a.outs) store_as(a.y, (int64_t)s * a.outs + j, 0.0f, a.y_type);
+        }
+        return;
+    }
     // the row of x of tile row i; rows that are none read row 0
     auto x_row = [&](int i) { return (int64_t)(max(slot_of[min(i, rows - 1)], 0) / a.top); };
     // the weight row of tile row i, past the last one the last one; with the
@@ -200,36 +229,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grouped_gemm_kernel(GgArgs a)
         }
         return (int64_t)min(j0 + i, a.outs - 1);
     };
-    // x is at most 4 GiB, so a row's place in it is a 32-bit offset; the weight
-    // rows of a tile follow each other (with the gate those of each half), so
-    // that one offset a thread does for them
+    // x is at most 4 GiB, so a row's place in it is a 32-bit offset
     uint32_t pa[CA];
 #pragma unroll
     for (int i = 0; i < CA; i++) pa[i] = (uint32_t)(x_row(row + i * RS) * rb);
     const __amdgpu_buffer_rsrc_t rA = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(a.xq), (short)0, (int)0xFFFFFFFF, 0x00020000);
-    const int wrows = min(COLS, a.outs - j0);
-    const __amdgpu_buffer_rsrc_t rB0 = mx_rsrc(w + j0 * rb, wrows * rb);
-    const __amdgpu_buffer_rsrc_t rB1 = mx_rsrc(w + (j0 + half) * rb, wrows * rb);
-    struct Regs {
-        u32x4 a[CA], b[CB];
-    };
-    // blocks past the row's end repeat its last one: their scales are 2^-127 on
-    // both sides, whose products vanish in any f32 sum
-    auto load = [&](Regs &R, int s, auto tes) {
-        const uint32_t at = 16u * (uint32_t)min(kGgBlocks * s + chunk, nblk - 1);
-        const uint32_t ob = (uint32_t)((GLU ? row & 31 : row) * rb) + at;
+    auto load_a = [&](Regs &R, int s, auto tes) {
+        const uint32_t at = offset(s);
 #pragma unroll
         for (int i = 0; i < CA * decltype(tes)::value / TM; i++) R.a[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rA, pa[i] + at, 0, 0));
-#pragma unroll
-        for (int i = 0; i < CB; i++) {
-            if constexpr (GLU && RS == 32) {
-                R.b[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(i & 1 ? rB1 : rB0, ob, (i >> 1) * 32 * (int)rb, 0));
-            } else if constexpr (GLU) {
-                R.b[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wave & 4 ? rB1 : rB0, ob, i * 32 * (int)rb, 0));
-            } else {
-                R.b[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rB0, ob, i * RS * (int)rb, 0));
-            }
-        }
     };
     const int at = row * kGgRowBytes + slot(row, chunk);
     auto store_a = [&](uint8_t *p, const Regs &R, auto tes) {
@@ -296,14 +304,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grouped_gemm_kernel(GgArgs a)
     // The tile's rows in 32 WM: the waves' share of x beyond them is left out.
     auto product = [&](auto tes) {
         constexpr int TE = decltype(tes)::value;
-        Regs R;
         ScaleRegs S;
         load_scales(S, 0);
-        load(R, 0, tes);
+        load_a(R, 0, tes);
         store_scales(S, 0);
         store_a(st[0], R, tes);
         store_b(st[0], R);
-        load(R, 1, tes);
+        load_a(R, 1, tes);
+        load_b(R, 1);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < TE; i++) {
@@ -367,7 +375,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grouped_gemm_kernel(GgArgs a)
             step(q2, q3, here);
             store_b(there, R);
             order(no, some);
-            load(R, s + 2, tes);
+            load_a(R, s + 2, tes);
+            load_b(R, s + 2);
             __syncthreads();
             step(q3, q0, there);
             order(yes, none);
