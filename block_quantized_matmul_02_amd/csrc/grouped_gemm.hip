@@ -11,8 +11,8 @@
 //    are gathered through the order, y's are scattered.
 //  * Rows come in any number: the waves that share a weight row take every
 //    other 32 rows of x, and a tile of fewer rows runs a loop with as many
-//    products as 64 rows need (32768 x 4096 x 2816 over 64 experts, 278 us;
-//    301 with whole tiles).
+//    products as 64 rows need (32768 x 4096 x 2816 over 64 experts, 278 us
+//    where whole tiles took 301).
 //  * With the gate a wave has weight rows of each half, so that the two meet in
 //    its registers.
 //  * Codes and scales go to v_mfma_scale_f32_32x32x64_f8f6f4 as they are
@@ -23,13 +23,17 @@
 //    its way fit a wave's 256 registers (one loop body a stage: an exit in the
 //    middle of two doubled the results' registers and spilled).
 //
-// Bound by the operands' way and the matrix cores together: 32768 slots of 64
-// experts, 4096 x 2816 with the gate, 278 us = 2.7 PFLOP/s; 240 without the
-// loads of the stages, 168 on constant operands and without stores.  Measured
-// and not kept there: 128-k stages with two workgroups a compute unit 342, two
-// stages in registers with 192-row tiles 294 (295 with one), a touch of the
-// lines three stages ahead 323 to 349.  Few rows an expert are bound by the
-// weights: 288 slots of 64 experts, 78 us (5.0 TB/s).
+// Bound by the operands' way and the clock: 32768 slots of 64 experts, 4096 x
+// 2816 with the gate, 266 us = 2.8 PFLOP/s (283 on a slower box; 240 of 279
+// without the stages' loads, 168 on constant operands and without stores; no
+// LDS conflicts, the matrix cores busy a third of the time at 2.0 GHz, 77% of
+// the requests hit L2).  7996 slots of 16, 1440 x 5120 to f32 75 us (32 of them
+// its 164 MB of results at the copy's rate).  Measured there and not kept:
+// 128-k stages with two workgroups a compute unit 342 (of 278), two stages in
+// registers with 192-row tiles 294 (of 295), a touch of the lines three stages
+// ahead 323 to 349, four waves of 128 x 128 336 (of 283), raised priority and
+// other places of the loads and LDS stores 284 to 286 (of 283).  Few rows an
+// expert are bound by the weights: 288 slots of 64 experts, 77 us (5.1 TB/s).
 #include <type_traits>
 
 #include "groups.h"
@@ -175,10 +179,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grouped_gemm_kernel(GgArgs a)
     const int half = GLU ? a.outs : 0;
 
     // row tid / 8 (+ RS per chunk) of each operand, 16-byte chunk tid % 8 of the
-    // stage, stored in a slot of its LDS row such that eight rows' reads of one
-    // chunk meet eight different slots
+    // stage, stored in a slot of its LDS row such that sixteen rows' reads of one
+    // chunk meet all of LDS's 64 banks: two rows fill them once, so it is every
+    // other row that takes the next slot
     const int chunk = tid & 7, row = tid >> 3;
-    auto slot = [](int r, int c) { return 16 * (c ^ (r & 7)); };
+    auto slot = [](int r, int c) { return 16 * (c ^ ((r >> 1) & 7)); };
     // Blocks past the row's end repeat its last one: their scales are 2^-127 on
     // both sides, whose products vanish in any f32 sum.
     auto offset = [&](int s) { return 16u * (uint32_t)min(kGgBlocks * s + chunk, nblk - 1); };

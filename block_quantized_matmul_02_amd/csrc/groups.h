@@ -52,6 +52,8 @@ __device__ __forceinline__ GroupTile find_group(const Grouping &q, int bm, int m
             GroupTile t;
             t.group = base + at;
             t.local = id - before - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(items, at));
+            // offsets that are none can make more items than 32 bits count
+            if ((unsigned)t.local >= (unsigned)__builtin_amdgcn_readlane(items, at)) break;
             t.first = __builtin_amdgcn_readlane(lo, at);
             t.rows = __builtin_amdgcn_readlane(rows, at);
             return t;

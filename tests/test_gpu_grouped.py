@@ -176,6 +176,21 @@ def test_grouped_gemm_bad_entries_are_passed_over(bqm):
     assert torch.equal(bqm.bqm_mxfp4_grouped_gemm(dev(w), dev(ws), dev(xq), dev(xs), ends, order), good)
 
 
+def test_grouped_gemm_offsets_that_are_none_touch_nothing_else(bqm):
+    """Groups that overlap, run backwards or all hold everything: whatever the outputs are, they stay in their tensor."""
+    rng = np.random.default_rng(9)
+    groups, k, n, slots = 300, 64, 34, 700
+    w, ws = random_mx((groups, n), k, rng)
+    xq, xs = random_mx((slots,), k, rng)
+    order = dev(rng.permutation(slots).astype(np.int32))
+    for kind in ("all", "backwards", "wild"):
+        offsets = {"all": np.arange(groups + 1) % 2 * slots, "backwards": np.linspace(slots, 0, groups + 1),
+                   "wild": rng.integers(-2 ** 31, 2 ** 31, groups + 1)}[kind].astype(np.int32)
+        wide = torch.full((slots + 2, n), 77.0, device=DEV)
+        bqm.bqm_mxfp4_grouped_gemm(dev(w), dev(ws), dev(xq), dev(xs), dev(offsets), order, y=wide[1:-1])
+        assert bool((wide[0] == 77).all()) and bool((wide[-1] == 77).all()) and bool(wide[1:-1].isfinite().all())
+
+
 def check_gemv(bqm, w, ws, x, ids, glu):
     k, slots = x.shape[1], len(ids)
     n = w.shape[1]

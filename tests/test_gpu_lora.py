@@ -182,6 +182,17 @@ def test_lora_add_bad_entries_are_passed_over(bqm):
     assert torch.equal(y[keep], good[keep]) and bool((y[lost] == 77).all())
 
 
+@pytest.mark.parametrize("m,adapters,r", [(1024, 16, 16), (1100, 3, 24), (3300, 4, 64), (1030, 2, 136), (6200, 2, 8), (12400, 1, 72)])
+def test_lora_add_many_rows(bqm, m, adapters, r):
+    """Adapters of many rows: 64 rows a workgroup, k in eight, four, two and one part."""
+    rng = np.random.default_rng(m)
+    for xt, abt in PAIRS:
+        x, a, b = make(m, 264, 70, r, adapters, xt, abt, seed=m)
+        ids = rng.integers(-1, adapters, m)
+        res = torch.randn((m, 70), generator=torch.Generator().manual_seed(1)).to(DEV)
+        check(bqm, x, a, b, ids, None, res, xt, abt)
+
+
 def test_lora_add_past_4_gib(bqm):
     """y of more than 2^31 values in a wide buffer: rows either side of the marks."""
     m, n, ldy = 70_000, 64, 33_000
