@@ -27,7 +27,7 @@ ARCH = "gfx950"
 
 SOURCES = ["q8_1_quantize.hip", "q8_0_gemv.hip", "q8_0_gemv_mma.hip", "q8_0_gemm.hip", "e4m3.hip", "e4m3_exact.hip", "e4m3_gemv.hip", "f16_mirror.hip", "e4m3_blk.hip", "norm.hip",
            "mxfp4_quantize.hip", "mxfp4_gemm.hip", "mxfp4_stream.hip", "mxfp4_gemv.hip", "logprobs.hip", "route.hip",
-           "grouped_gemm.hip", "expert_gemv.hip", "combine.hip", "lora.hip", "strerror.cpp"]
+           "grouped_gemm.hip", "grouped_stream.hip", "expert_gemv.hip", "combine.hip", "lora.hip", "strerror.cpp"]
 
 HIPFLAGS = [
     f"--offload-arch={ARCH}",
@@ -49,6 +49,7 @@ EXTRA = {
     "e4m3_blk.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "mxfp4_stream.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "mxfp4_gemv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "grouped_stream.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "expert_gemv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "lora.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }

@@ -36,18 +36,9 @@
 // expert are bound by the weights: 288 slots of 64 experts, 77 us (5.1 TB/s).
 #include <type_traits>
 
-#include "groups.h"
+#include "grouped_gemm.h"
 
 namespace bqm {
-
-struct GgArgs {
-    const uint8_t *w, *ws, *xq, *xs;
-    void *y;
-    Grouping q;
-    int y_type, top;
-    int k, n, outs;      // outs: columns of y
-    int ntiles;
-};
 
 template <int Q>
 __device__ __forceinline__ v16f gg_mfma(u32x4 a, u32x4 b, v16f c, int sa, int sb) {
@@ -55,36 +46,6 @@ __device__ __forceinline__ v16f gg_mfma(u32x4 a, u32x4 b, v16f c, int sa, int sb
     const v8i vb = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
     // formats 4, 4: e2m1 on both sides; scale byte Q of each scale dword
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(va, vb, c, 4, 4, Q, sa, Q, sb);
-}
-
-// The 16 scale bytes from block b0 on of the row of nblk bytes at p, at any
-// alignment; zeros past its end.
-__device__ __forceinline__ void scale_bytes(const uint8_t *p, int b0, int nblk, unsigned (&v)[4]) {
-    if (nblk >= 16) {
-        const int from = min(b0, nblk - 16), shift = b0 - from;   // uniform
-        u32x4 u;
-        __builtin_memcpy(&u, p + from, 16);
-#pragma unroll
-        for (int e = 0; e < 4; e++) v[e] = u[e];
-        if (shift > 0) {
-#pragma unroll
-            for (int d = 2; d >= 1; d /= 2)
-                if ((shift >> 2) & d) {
-#pragma unroll
-                    for (int q = 0; q < 4; q++) v[q] = q + d < 4 ? v[q + d] : 0;
-                }
-#pragma unroll
-            for (int q = 0; q < 4; q++) v[q] = __builtin_amdgcn_alignbyte(q < 3 ? v[q + 1] : 0, v[q], shift & 3);
-        }
-    } else {
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-            v[q] = 0;
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-                if (4 * q + e < nblk - b0) v[q] |= (unsigned)p[b0 + 4 * q + e] << (8 * e);
-        }
-    }
 }
 
 // Workgroups reach the eight XCDs round-robin; of each 256 consecutive ones (a
@@ -422,11 +383,15 @@ static int launch_gg(GgArgs a, hipStream_t s) {
 // Measured (large, small; us): 32768 x 4096 x 2816 of 64 278, 343; 4096 x 4096
 // x 2816 of 16 62, 54; 2048 x 4096 x 4096 of 8 41, 45; 1024 x 2048 x 2048 of 16
 // 20.5, 16.4; 64 slots x 1024 x 4096 of 16 12.2, 11.7; 32 x 4096 x 1024 of 8 17.4, 14.8.
+// Where the small ones leave half of the card idle and k is long, waves that
+// share k may do better (grouped_stream.hip).
 template <bool GLU>
 static int launch_gg_by_rows(const GgArgs &a, hipStream_t s) {
     const int64_t used = a.q.groups < a.q.slots ? a.q.groups : a.q.slots;
     const int64_t small = (a.q.slots / 128 + (used + 1) / 2) * (((int64_t)a.n + 127) / 128);
-    return small <= 2 * device_cus() ? launch_gg<2, 2, 2, 2, GLU>(a, s) : launch_gg<2, 4, 4, 2, GLU>(a, s);
+    const int cus = device_cus();
+    if (grouped_stream_applies(a, small, cus)) return grouped_stream(a, cus, s);
+    return small <= 2 * cus ? launch_gg<2, 2, 2, 2, GLU>(a, s) : launch_gg<2, 4, 4, 2, GLU>(a, s);
 }
 
 }  // namespace bqm

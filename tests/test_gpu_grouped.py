@@ -78,6 +78,8 @@ SHAPES = [  # rows, top, groups, k, n
     (1, 1, 1, 32, 2), (1, 2, 4, 64, 34), (3, 2, 5, 96, 66), (16, 4, 8, 288, 130), (40, 2, 3, 1024, 64),
     (65, 3, 4, 1056, 258), (7, 8, 64, 2048, 96), (200, 1, 3, 512, 514), (333, 2, 2, 1440, 320), (130, 6, 100, 544, 190),
     (20, 1, 1024, 256, 36), (500, 4, 1, 128, 70), (64, 8, 16, 4128, 128), (300, 4, 16, 800, 1030),
+    # few tiles and long rows: the kernel whose waves share k
+    (16, 2, 8, 4096, 130), (5, 3, 4, 8224, 66), (33, 1, 2, 16416, 50), (100, 1, 2, 2080, 200), (1, 3, 4, 4064, 34),
     # more tiles of 128 x 128 than a card takes at once: the large tile
     (300, 2, 64, 544, 2080), (1500, 1, 5, 800, 5150), (700, 2, 3, 288, 6002), (90, 1, 90, 1056, 1602),
 ]
@@ -124,10 +126,10 @@ def test_grouped_gemm_every_count_of_rows(bqm, n, glu):
         check_gemm(bqm, w, ws, xq, xs, ids, glu, t)
 
 
-@pytest.mark.parametrize("rows,top,groups,n", [(24, 4, 8, 200), (400, 2, 4, 200), (1500, 2, 3, 200), (1500, 2, 3, 2600)])
-def test_grouped_gemm_a_slots_bits_do_not_depend_on_the_others(bqm, rows, top, groups, n):
+@pytest.mark.parametrize("rows,top,groups,n,k", [(24, 4, 8, 200, 1056), (24, 4, 8, 200, 5152), (400, 2, 4, 200, 1056),
+                                                 (1500, 2, 3, 200, 1056), (1500, 2, 3, 2600, 1056)])
+def test_grouped_gemm_a_slots_bits_do_not_depend_on_the_others(bqm, rows, top, groups, n, k):
     rng = np.random.default_rng(8)
-    k = 1056
     w, ws = random_mx((groups, n), k, rng, 100, 150)
     xq, xs = random_mx((rows,), k, rng, 100, 150)
     ids = rng.integers(0, groups, rows * top)
@@ -138,7 +140,7 @@ def test_grouped_gemm_a_slots_bits_do_not_depend_on_the_others(bqm, rows, top, g
     assert torch.equal(a[kept].view(torch.int32), b[kept].view(torch.int32))
 
 
-@pytest.mark.parametrize("k", [32, 96, 800, 1024, 1056, 1440])
+@pytest.mark.parametrize("k", [32, 96, 800, 1024, 1056, 1440, 4128, 8192])
 def test_grouped_gemm_nan_scales_stay_with_their_rows(bqm, k):
     """A scale byte 255 makes its slot or weight row NaN, and nothing beside it: not the rows whose scales follow."""
     rng = np.random.default_rng(k)

@@ -5,7 +5,7 @@ import pytest
 
 from test_kernel_code import assembly
 
-SOURCES = ["route.hip", "grouped_gemm.hip", "expert_gemv.hip", "combine.hip", "lora.hip"]
+SOURCES = ["route.hip", "grouped_gemm.hip", "grouped_stream.hip", "expert_gemv.hip", "combine.hip", "lora.hip"]
 
 
 @pytest.mark.parametrize("source", SOURCES)
