@@ -24,7 +24,7 @@
 //    middle of two doubled the results' registers and spilled).
 //
 // Bound by the operands' way and the clock: 32768 slots of 64 experts, 4096 x
-// 2816 with the gate, 266 us = 2.8 PFLOP/s (283 on a slower box; 240 of 279
+// 2816 with the gate, 266 us = 2.8 PFLOP/s (283 on another card; 240 of 279
 // without the stages' loads, 168 on constant operands and without stores; no
 // LDS conflicts, the matrix cores busy a third of the time at 2.0 GHz, 77% of
 // the requests hit L2).  7996 slots of 16, 1440 x 5120 to f32 75 us (32 of them

@@ -155,6 +155,30 @@ def test_grouped_gemm_nan_scales_stay_with_their_rows(bqm, k):
     assert np.array_equal(y, want)
 
 
+@pytest.mark.parametrize("rows,n,k", [(40, 70, 1056), (40, 70, 4128), (300, 6200, 544)])
+def test_grouped_gemm_every_scale_byte(bqm, rows, n, k):
+    """Scale bytes over their whole range, those of a block's two sides near a sum of 254, so that results are near 1;
+    k ends inside a stage, and what stands there must not count."""
+    rng = np.random.default_rng(k)
+    groups = 3
+    w, xq = (rng.integers(0, 256, shape).astype(np.uint8) for shape in ((groups, n, k // 2), (rows, k // 2)))
+    at = rng.permutation(np.arange(k // 32) * 254 // (k // 32 - 1))
+    xs = np.clip(at[None, :] + rng.integers(-2, 3, (rows, k // 32)), 0, 254).astype(np.uint8)
+    ws = np.clip(254 - at[None, None, :] + rng.integers(-2, 3, (groups, n, k // 32)), 0, 254).astype(np.uint8)
+    check_gemm(bqm, w, ws, xq, xs, rng.integers(0, groups, rows), False)
+
+
+@pytest.mark.parametrize("k", [1056, 8160])
+def test_expert_gemv_every_scale_byte(bqm, k):
+    rng = np.random.default_rng(k)
+    w = rng.integers(0, 256, (2, 50, k // 2)).astype(np.uint8)
+    at = rng.permutation(np.arange(k // 32) * 252 // (k // 32 - 1))
+    ws = np.clip(at[None, None, :] + rng.integers(-2, 3, (2, 50, k // 32)), 0, 252).astype(np.uint8)
+    # x of a block brings its terms near 1, as far as its own bits reach
+    x = rng.standard_normal((6, k)) * np.exp2(np.clip(127.0 - np.repeat(at, 32), -100, 120))
+    check_gemv(bqm, w, ws, x.astype(np.float32), np.array([0, 1, 0, 0, 1, 1]), False)
+
+
 def test_grouped_gemm_bad_entries_are_passed_over(bqm):
     """Order entries and offsets outside the slots lead nowhere: the good rows come out right, nothing else is touched."""
     rng = np.random.default_rng(4)
