@@ -190,3 +190,29 @@ def test_combine_unaligned_rows(bqm):
     w = torch.rand((4, 2), generator=torch.Generator().manual_seed(3)).to(DEV)
     a, b = flat[1:].view(8, 64), flat[1:].clone().view(8, 64)
     assert torch.equal(bqm.bqm_combine(a, w), bqm.bqm_combine(b, w))
+
+
+@pytest.mark.parametrize("top", [1, 3, 9])
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("same", [False, True])
+def test_combine_ragged_rows_in_place(bqm, top, t, same):
+    """Rows of every rest of 16 bytes, from bases that are aligned to an element only, in place and not, and what lies
+    on either side of out."""
+    m, ot = 5, t if same else torch.float32
+    for n in list(range(1, 26)) + [1029, 2055]:
+        g = torch.Generator().manual_seed(n)
+        y = torch.randn(m * top * n + 1, generator=g).to(t).to(DEV)[1:].view(m * top, n)
+        w = torch.rand((m, top), generator=g).to(DEV)
+        res = torch.randn((m, n), generator=g).to(ot).to(DEV)
+        flat = torch.full((m * n + 16,), 77.0, dtype=ot, device=DEV)
+        out = flat[1:1 + m * n].view(m, n)
+        bqm.bqm_combine(y, w, res, out=out)
+        want, total = combine_ref(y, w, res, m, top)
+        sums = (top + 1) * 2.0 ** -24 * total                # a rounding of 2^-24 of the terms' sum each
+        tol = sums + (0 if ot == torch.float32 else groups_ref.half_step(np.abs(want) + sums, torch.finfo(ot).eps, 2.0 ** -24 if ot == torch.float16 else 2.0 ** -133))
+        assert (np.abs(out.cpu().double().numpy() - want) <= tol).all(), n
+        assert bool((flat[:1] == 77).all()) and bool((flat[1 + m * n:] == 77).all()), n
+        kept = out.clone()
+        out.copy_(res)
+        assert bqm.bqm_combine(y, w, out, out=out) is out and torch.equal(out, kept), n
+        assert bool((flat[:1] == 77).all()) and bool((flat[1 + m * n:] == 77).all()), n
