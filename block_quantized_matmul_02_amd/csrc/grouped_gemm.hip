@@ -159,15 +159,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grouped_gemm_kernel(GgArgs a)
     const __amdgpu_buffer_rsrc_t rB1 = mx_rsrc(w + (j0 + half) * rb, wrows * rb);
     auto load_b = [&](Regs &R, int s) {
         const uint32_t ob = (uint32_t)((GLU ? row & 31 : row) * rb) + offset(s);
+        // the row step stays in the per-lane offset, which the range check
+        // covers: the scalar offset is added past it, and a ragged tile's rows
+        // past the last would be read
 #pragma unroll
         for (int i = 0; i < CB; i++) {
-            if constexpr (GLU && RS == 32) {
-                R.b[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(i & 1 ? rB1 : rB0, ob, (i >> 1) * 32 * (int)rb, 0));
-            } else if constexpr (GLU) {
-                R.b[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wave & 4 ? rB1 : rB0, ob, i * 32 * (int)rb, 0));
-            } else {
-                R.b[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rB0, ob, i * RS * (int)rb, 0));
-            }
+            const uint32_t step = (uint32_t)((GLU ? (RS == 32 ? i >> 1 : i) * 32 : i * RS) * rb);
+            const __amdgpu_buffer_rsrc_t rB = !GLU ? rB0 : (RS == 32 ? i & 1 : wave & 4) ? rB1 : rB0;
+            R.b[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rB, ob + step, 0, 0));
         }
     };
     // the first weights are on their way while the slots are looked up
