@@ -314,6 +314,8 @@ extern "C" int bqm_mxfp4_expert_gemv(const uint8_t *w, const uint8_t *ws, const 
     if (rows < 1 || slots < 1 || slots > BQM_EXPERT_GEMV_MAX_SLOTS || slots % rows != 0) return BQM_EINVAL;
     if (groups < 1 || groups > BQM_MAX_GROUPS || k < 32 || n < 1 || (glu && n % 2 != 0)) return BQM_EINVAL;
     if (k % 32 != 0 || k > BQM_EXPERT_GEMV_MAX_K) return BQM_EUNSUPPORTED;
+    // whole units, as many as loads and loops look ahead, in 31 bits (half of n with the gate)
+    if (!glu && n > 0x7FFFFFFF - 4 * kEvWaves * 32) return BQM_EUNSUPPORTED;
     if (!aligned(w, 16) || !aligned(x, 16) || !aligned(ids, 4) || !aligned(y, 4)) return BQM_EUNSUPPORTED;
     const bool wide = k % 128 == 0 && aligned(ws, 4);
     static LaunchCache caches[2];
