@@ -399,9 +399,11 @@ extern "C" int bqm_lora_add(const void *x, int64_t ldx, int x_type, const void *
     if (!aligned(scale, 4) || !aligned(offsets, 4) || !aligned(order, 4) || !aligned(res, 4) || !aligned(y, 4)) return BQM_EUNSUPPORTED;
     if (res == y && ldr != ldy) return BQM_EUNSUPPORTED;
     const int group = lora_group(m, adapters);
-    const int64_t tiles = most_tiles(m, adapters, 16), strips = ((int64_t)n + kExpandStrip - 1) / kExpandStrip;
-    // what a dispatch counts, and an adapter in 31 bits
-    if (tiles > 65535 || tiles * strips * 512 > 0x7FFFFFFFll || tiles * 128 * 512 > 0x7FFFFFFFll || k > 1 << 21) return BQM_EUNSUPPORTED;
+    // The expand's grid, of tiles in y, in what a dispatch counts, and an adapter
+    // in 31 bits.  The shrink's is smaller: 16 parts of the ranks times 8 of k
+    // are for few rows, and many rows have one part of k.
+    const int64_t tiles = most_tiles(m, adapters, group > 1 ? 32 : 16), strips = ((int64_t)n + kExpandStrip - 1) / kExpandStrip;
+    if (tiles > 65535 || tiles * strips * 512 > 0x7FFFFFFFll || k > 1 << 21) return BQM_EUNSUPPORTED;
     LoraArgs q = {{offsets, order, adapters, m}, x, ldx, a, b, scale, res, ldr, y, ldy, static_cast<float *>(workspace),
                   k, n, r, (r + 15) / 16 * 16, lora_splits(m, group), 0};
     q.range = (((k + q.splits - 1) / q.splits) + 127) / 128 * 128;

@@ -157,8 +157,10 @@ int bqm_combine(const void *y, int y_type, const float *weights, const void *res
  *   workspace : bqm_lora_add_workspace(m, r) bytes, 16-byte aligned; needs no
  *             initial contents.
  *   m, n, k >= 1, 1 <= r <= BQM_LORA_MAX_RANK, 1 <= adapters <=
- *   BQM_MAX_GROUPS (else BQM_EINVAL); k % 8 == 0, r % 8 == 0 (else
- *   BQM_EUNSUPPORTED).
+ *   BQM_MAX_GROUPS (else BQM_EINVAL); k % 8 == 0, r % 8 == 0, k <= 2^21 and,
+ *   with t = m / 16 + min(m, adapters + 1), or m / 32 + min(m, adapters + 1)
+ *   from 1024 rows and 64 for each adapter on, t <= 65535 and t * (n rounded
+ *   up to 512) < 2^31 (else BQM_EUNSUPPORTED).
  * An infinity or NaN in a row of x makes that row infinite or NaN where its
  * adapter reaches.  Bits of x or h below 2^-133 are lost.  A row's result does
  * not depend on the other rows.
@@ -167,7 +169,7 @@ int bqm_lora_add(const void *x, int64_t ldx, int x_type, const void *a, const vo
                  const int *offsets, const int *order, const float *res, int64_t ldr, float *y, int64_t ldy,
                  void *workspace, int m, int k, int n, int r, int adapters, void *stream);
 
-/* Bytes of workspace for bqm_lora_add, -1 for sizes it refuses. */
+/* Bytes of workspace for bqm_lora_add; -1 for m < 1 and r outside 1..BQM_LORA_MAX_RANK. */
 int64_t bqm_lora_add_workspace(int m, int r);
 
 #ifdef __cplusplus

@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 
 import layer_ref
+import test_gpu_lora as lora
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +56,12 @@ def test_expert_gemv_the_most_weight_rows(bqm, glu, n):
     rest = y[0]
     rest[at.to(DEV)] = float(rest[3])
     assert float(rest.max()) == float(rest.min()) and abs(float(rest[3]) - want) <= 200 * 2.0 ** -23 * np.abs(x[0]).sum() / 32 * (1 + abs(ones))
+
+
+@pytest.mark.parametrize("m,adapters,k,n,r,xt,abt", [(600_001, 40, 64, 70, 24, "bf16", "bf16"), (2_097_087, 1, 16, 5, 8, "f32", "f16")])
+def test_lora_add_the_most_rows(bqm, m, adapters, k, n, r, xt, abt):
+    """More than the half million rows that any rank and width once had to keep below, and as many as a grid has."""
+    rng = np.random.default_rng(m)
+    x, a, b = lora.make(m, k, n, r, adapters, xt, abt)
+    res = torch.randn((m, n), generator=torch.Generator().manual_seed(1)).to(DEV)
+    lora.check(bqm, x, a, b, rng.integers(-1, adapters, m), None, res, xt, abt)
