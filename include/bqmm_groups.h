@@ -55,7 +55,7 @@ extern "C" {
  *                element.
  *   ids        : int32 [m][top] out;  weights : f32 [m][top] out.
  *   m >= 1, 1 <= e <= BQM_MAX_GROUPS, 1 <= top <= min(e, BQM_MAX_TOP) (else
- *   BQM_EINVAL).
+ *   BQM_EINVAL); m <= 2^25 - 4 (else BQM_EUNSUPPORTED).
  */
 int bqm_route(const void *logits, int64_t ld, int type, int top, int renorm, int *ids, float *weights, int m, int e,
               void *stream);
@@ -95,7 +95,9 @@ int64_t bqm_group_rows_workspace(int count, int groups);
  *             f32 result is rounded once.
  *   rows, slots, n >= 1, slots a multiple of rows, 1 <= groups <=
  *   BQM_MAX_GROUPS, k >= 32, n even with glu (else BQM_EINVAL); k % 32 == 0;
- *   w and xq 16-byte aligned; xq less than 4 GiB (else BQM_EUNSUPPORTED).
+ *   w and xq 16-byte aligned; xq less than 4 GiB; k <= 2^22; and
+ *   (slots / 256 + min(slots, groups + 1)) * (n / 256, rounded up) < 2^22
+ *   (else BQM_EUNSUPPORTED).
  * Scales as in bqm_mxfp4_gemm.  The order of the sums depends on the sizes, on
  * none of the rows: a slot's result does not depend on the other slots.
  */
@@ -107,8 +109,11 @@ int bqm_mxfp4_grouped_gemm(const uint8_t *w, const uint8_t *ws, const uint8_t *x
  * The decode / verify form: few slots, f32 activations, experts by their ids
  * as bqm_route writes them, no grouping needed.  With bqm_mxfp4_gemv's sums
  *   p[s][r] = sum_b 2^(ws - 127) sum_{i in b} x[s / (slots / rows)][i] e2m1(w[ids[s]][r]),
- * y as bqm_mxfp4_grouped_gemm, in f32.  An expert's weights are read once for
- * up to five of its slots.  A slot's result does not depend on the others.
+ * y as bqm_mxfp4_grouped_gemm, in f32.  A workgroup takes up to five slots of
+ * an expert, as many as the sizes let one expect (one where rows == 1, about
+ * twice slots / groups otherwise); an expert of more is read by several, the
+ * later ones mostly from the caches.  A slot's result does not depend on the
+ * others.
  *
  *   x   : f32 [rows][k], 16-byte aligned, dense.
  *   ids : int32 [slots]; a slot whose id is outside 0..groups-1 gets zeros.
@@ -132,7 +137,8 @@ int bqm_mxfp4_expert_gemv(const uint8_t *w, const uint8_t *ws, const float *x, c
  *   out     : out_type [m][n] out, dense; may be res.  out_type is BQM_F32 or
  *             y_type (else BQM_EUNSUPPORTED).
  *   m, n >= 1, 1 <= top <= BQM_MAX_TOP (else BQM_EINVAL).  Every pointer is
- *   aligned to its element (else BQM_EUNSUPPORTED).
+ *   aligned to its element; with v = 4 for y of f32 and 8 for 16 bits,
+ *   m * (n / v, rounded up) < 2^31 - 255 (else BQM_EUNSUPPORTED).
  */
 int bqm_combine(const void *y, int y_type, const float *weights, const void *res, void *out, int out_type, int m,
                 int top, int n, void *stream);
