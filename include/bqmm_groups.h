@@ -86,6 +86,7 @@ int64_t bqm_group_rows_workspace(int count, int groups);
  *   glu == 0: y[s][r] = p[s][r], r < n;
  *   glu != 0: y[s][j] = p[s][j] / (1 + exp(-p[s][j])) * p[s][n/2 + j],
  *             j < n/2: the gate's weight rows stand before the other half.
+ *             A gate of -inf gives NaN, as the formula does.
  * A slot of no group gets zeros.
  *
  *   w, ws   : codes [groups][n][k/2] and scales [groups][n][k/32].
