@@ -65,3 +65,29 @@ def test_lora_add_the_most_rows(bqm, m, adapters, k, n, r, xt, abt):
     x, a, b = lora.make(m, k, n, r, adapters, xt, abt)
     res = torch.randn((m, n), generator=torch.Generator().manual_seed(1)).to(DEV)
     lora.check(bqm, x, a, b, rng.integers(-1, adapters, m), None, res, xt, abt)
+
+
+# tiles of 256 rows; of 128 (the most bytes of x); of 256 at that; the waves that share k
+@pytest.mark.parametrize("rows,k,n", [(900_001, 8192, 64), (8191, 2 ** 20, 32), (8191, 2 ** 20, 1100), (5000, 2 ** 20, 32)])
+def test_grouped_gemm_x_past_2_gib(bqm, rows, k, n):
+    """x of 2.6 to 4.3 GB.  A row of x has one block that is not zeros, so its sums are exact: rows either side of 2 GiB,
+    the last ones and others."""
+    nblk = k // 32
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    w = torch.randint(0, 256, (1, n, k // 2), generator=g, device=DEV, dtype=torch.uint8)
+    ws = torch.randint(120, 134, (1, n, nblk), generator=g, device=DEV, dtype=torch.uint8)
+    xq = torch.zeros((rows, nblk, 16), dtype=torch.uint8, device=DEV)
+    xs = torch.full((rows, nblk), 127, dtype=torch.uint8, device=DEV)
+    block = torch.arange(rows, device=DEV) * 7919 % nblk
+    codes = torch.randint(0, 256, (rows, 16), generator=g, device=DEV, dtype=torch.uint8)
+    xq[torch.arange(rows, device=DEV), block] = codes
+    offsets = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    order = torch.randperm(rows, generator=g, device=DEV).int()
+    y = bqm.bqm_mxfp4_grouped_gemm(w, ws, xq.view(rows, k // 2), xs, offsets, order)
+    mark = 2 ** 31 // (k // 2)
+    at = sorted({0, 1, mark - 1, mark, mark + 1, rows - 2, rows - 1, *np.random.default_rng(k).integers(0, rows, 120).tolist()})
+    for r in at:
+        b = int(block[r])
+        v = layer_ref.mxfp4_values(w[0, :, 16 * b:16 * b + 16].cpu().numpy(), ws[0, :, b:b + 1].cpu().numpy())
+        x = layer_ref.mxfp4_values(codes[r:r + 1].cpu().numpy(), np.full((1, 1), 127, np.uint8))[0]
+        assert np.array_equal(y[r].cpu().double().numpy(), v @ x), r
