@@ -8,8 +8,9 @@
 // bytes and stores the values that are its own (res may be out, so the others'
 // are neither read nor stored).
 //
-// Measured, in a graph: 4001 x 8 x 5120 bf16 69.2 us (5.3 TB/s, what a large
-// copy reaches); 4001 x 8 x 5121 75.1 (95.1 value by value), 5068 x 1 x 2529
+// Measured, in a graph: 4001 x 8 x 5120 bf16 69 to 72 us (5.3 TB/s, what a
+// large copy reaches), x 10, whose second turn loads its last slot again, 86
+// (88 at the copy's rate); 4001 x 8 x 5121 75.1 (95.1 value by value), 5068 x 1 x 2529
 // f32 21.2 (44.6 value by value and with eight loads of the one slot, so J is
 // 1, 4 or 8), 3000 x 2 x 4100 f16 to f32 31.0 (52.8); 8 x 8 x 4097 f32, all
 // latency, 2.7 (2.4).

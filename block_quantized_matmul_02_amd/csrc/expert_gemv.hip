@@ -17,15 +17,17 @@
 //    several waves share its slices and their sums meet in LDS, added in wave
 //    order.  Weights stream a slice of both tiles ahead and pass through a
 //    wave's own LDS tile, 256 contiguous bytes a row from memory.
-//  * Two workgroups of eight waves a compute unit: one starts (ids, x) while
-//    the other streams.  One a compute unit, with two slices ahead, took 54 us
-//    instead of 35 at 54 slots of 64 experts, 1408 x 4096, and 145 instead of
-//    60 at 48 of 60, 5120 x 3328.
+//  * Two workgroups of eight waves a compute unit, where their operands fit:
+//    one starts (ids, x) while the other streams.  One a compute unit, with two
+//    slices ahead, took 54 us instead of 35 at 54 slots of 64 experts, 1408 x
+//    4096.
 //
-// Weights from HBM, in a graph: 8 slots of 64 experts, 4096 x 2816 with the
-// gate, 16 us (49 MB: 9.6 at 5.1 TB/s; ids, x and the first weights are three
-// trips to memory that follow each other), 54 slots, 1408 x 4096, 35 us (22.7),
-// 48 of 60, 5120 x 3328 with the gate, 60 us (at the copy's rate).
+// In a graph: 8 slots of 64 experts, 4096 x 2816 with the gate, 15.4 us (49 MB:
+// 9.6 at 5.1 TB/s; 176 workgroups, and ids, x and the first weights are three
+// trips to memory that follow each other), 54 slots of 35 distinct of 64, 1408
+// x 4096, 32.4 us (20.7; two units a wave), 48 of 32 distinct of 60, 5120 x
+// 3328 with the gate, 85 us (57; two slots' operand is 113 KB of LDS, one
+// workgroup a compute unit).
 #include "groups.h"
 
 namespace bqm {
@@ -333,9 +335,11 @@ extern "C" int bqm_mxfp4_expert_gemv(const uint8_t *w, const uint8_t *ws, const 
         for (int i = 0; i < slots; i++) missed *= 1.0 - 1.0 / groups;
         distinct = groups * (1.0 - missed);
     }
-    // Waves share k as far as there are fewer units than four a compute unit
-    // (8 slots, 4096 x 2816: 15.6 us with four waves a unit, 22 with one, 17.8
-    // with eight; 4 x 4, 2048 x 1536: 10.5 with four, 12.8 with one).
+    // Waves share k as far as there are fewer units than four a compute unit.
+    // In a graph (us; one, two, four, eight waves a unit): 8 slots, 4096 x 2816
+    // with the gate 22.2, 15.4 (taken), 16.2, 17.7; 4 of 4, 2048 x 1536 12.4,
+    // 9.0, 7.4 (taken); 54 of 64, 1408 x 4096 32.9 (taken), 34.2, and 38.3 with
+    // three; 48 of 60, 5120 x 3328 with the gate 83.8 (taken), 84.4, 91.9, 107.
     a.parts = 1;
     while (distinct * units * a.parts < 4.0 * cus && a.parts < kEvWaves && a.parts < a.slices) a.parts *= 2;
     if (a.parts > a.slices) a.parts = a.slices;

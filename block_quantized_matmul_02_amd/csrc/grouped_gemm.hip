@@ -24,11 +24,13 @@
 //    middle of two doubled the results' registers and spilled).
 //
 // Bound by the operands' way and the clock: 32768 slots of 64 experts, 4096 x
-// 2816 with the gate, 266 us = 2.8 PFLOP/s (283 on another card; 240 of 279
-// without the stages' loads, 168 on constant operands and without stores; no
-// LDS conflicts, the matrix cores busy a third of the time at 2.0 GHz, 77% of
-// the requests hit L2).  7996 slots of 16, 1440 x 5120 to f32 75 us (32 of them
-// its 164 MB of results at the copy's rate).  Measured there and not kept:
+// 2816 with the gate, 282 us = 2.7 PFLOP/s (266 to 286 by card and clock; 240
+// of 279 without the stages' loads, 168 on constant operands and without
+// stores; no LDS conflicts, 78% of the requests hit L2; the matrix cores are
+// busy 34% of the launch's cycles, 95 us at 2.0 GHz, and 40% of those in which
+// their compute unit had work).  7996 slots of 16, 1440 x 5120 to f32 76 us (72
+// to 80; 32 of them its 164 MB of results at the copy's rate, and some 780 tiles
+// are three rounds on 256 compute units and a few more).  Not kept, on the first:
 // 128-k stages with two workgroups a compute unit 342 (of 278), two stages in
 // registers with 192-row tiles 294 (of 295), a touch of the lines three stages
 // ahead 323 to 349, four waves of 128 x 128 336 (of 283), raised priority and

@@ -22,8 +22,10 @@
 //    (56), as were 64 rows a workgroup (55) and accesses past the caches (63).
 //
 // In a graph: 1 x 4096 x 16 x 4096 6.9 us, 64 rows of 40 adapters, 4096 x 16 x
-// 20480 14.5 us (36 MB; 7.2 at 5.1 TB/s), 4099 rows of 6, 4096 x 64 x 5152 in
-// fp16 16 + 50 us (33.6 and 169 MB; 40 in all).
+// 20480 14.7 us (36 MB; 7.2 at 5.1 TB/s; some 1300 workgroups of the expand,
+// each of 24 KB behind offsets, order, h and a barrier), 4099 rows of 6, 4096 x
+// 64 x 5152 in fp16 16 + 54 us (33.6 and 169 MB; 40 in all), of f32 rows and
+// bf16 adapters 25 + 52 (67 and 169 MB; 47).
 #include "groups.h"
 
 namespace bqm {

@@ -13,8 +13,11 @@
 //    order, so that a row's place is (rows of lower groups) + (rows of its
 //    group in earlier chunks, waves, batches and lanes): no atomics, the same
 //    order every time.  Equal ids of a wave are found by a ballot for each bit
-//    of the id.  More rows take two launches, the chunks' counts in between;
-//    at most 64 take a wave that compares them with each other.
+//    of the id.  More rows take two launches, the chunks' counts in between,
+//    of which each workgroup reads all: right up to 2^24 rows, but the time
+//    grows with the square of the chunks (256 groups, 65536 rows 9.6 us, 2^20
+//    56, 2^22 440; 2^24 of 1024 32 ms).  At most 64 take a wave that compares
+//    them with each other.
 //
 // In a graph: 1 x 128, 8 of them, and their sort 4.6 us (two launches); 8192 x
 // 256 and the sort of 65536 rows 16.5: 8 (the choice: 25 instructions a turn
