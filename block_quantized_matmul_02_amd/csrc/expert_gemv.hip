@@ -95,7 +95,7 @@ __global__ __launch_bounds__(kEvWaves * 64, 4) void expert_gemv_kernel(EvArgs a)
     const int slot0 = blockIdx.y;
     const int outs = a.glu ? a.n / 2 : a.n;
     const int per_unit = a.glu ? 16 : 32;                   // outputs of a unit
-    const int units = (outs + per_unit - 1) / per_unit;
+    const int units = (outs - 1) / per_unit + 1;            // n may be the most that 31 bits hold
     const int unit0 = blockIdx.x * a.each, unit1 = min(unit0 + a.each, units);
     if (unit0 >= unit1) return;
 
@@ -107,8 +107,9 @@ __global__ __launch_bounds__(kEvWaves * 64, 4) void expert_gemv_kernel(EvArgs a)
     for (int j = 0; j < BQM_EXPERT_GEMV_MAX_SLOTS / 64; j++)
         if (slot0 >> 6 == j) expert = __builtin_amdgcn_readlane(all[j], slot0 & 63);
     if ((unsigned)expert >= (unsigned)a.groups) {
-        const int lo = unit0 * per_unit, hi = min(unit1 * per_unit, outs);
-        for (int i = lo + tid; i < hi; i += blockDim.x) a.y[(int64_t)slot0 * outs + i] = 0.0f;
+        const int lo = unit0 * per_unit;
+        const unsigned cols = (unsigned)min((int64_t)(unit1 - unit0) * per_unit, (int64_t)outs - lo);
+        for (unsigned i = tid; i < cols; i += blockDim.x) a.y[(int64_t)slot0 * outs + lo + i] = 0.0f;
         return;
     }
     int count = 0, before = 0;
@@ -150,7 +151,7 @@ __global__ __launch_bounds__(kEvWaves * 64, 4) void expert_gemv_kernel(EvArgs a)
         const int blk0 = (wpart + a.parts * next_s) * kEvBlocks;
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            const int j0 = next_unit * per_unit + (a.glu ? 0 : 16 * h);
+            const int j0 = (int)((unsigned)next_unit * per_unit) + (a.glu ? 0 : 16 * h);   // of units past the last, any
             const int64_t row0 = j0 + (a.glu ? (int64_t)h * outs : 0);
             const int rows = next_unit < unit1 ? min(outs - j0, 16) : 0;   // may be <= 0: nothing is read
             const __amdgpu_buffer_rsrc_t rw = mx_rsrc(w + row0 * row_bytes, rows * row_bytes);
@@ -277,8 +278,9 @@ __global__ __launch_bounds__(kEvWaves * 64, 4) void expert_gemv_kernel(EvArgs a)
         const int per = per_unit * count;
         for (int o = tid; o < per * a.subs; o += blockDim.x) {
             const int su = o / per, in = o - su * per, tok = in / per_unit, col = in - tok * per_unit;
+            if (unit + su >= unit1) continue;
             const int j = (unit + su) * per_unit + col;
-            if (unit + su >= unit1 || j >= outs) continue;
+            if (j >= outs) continue;
             auto total = [&](int h, int c) {
                 const float2 *const q0 = out + (su * a.parts * 2 + h) * 64;
                 float sum = 0.0f;
@@ -316,8 +318,6 @@ extern "C" int bqm_mxfp4_expert_gemv(const uint8_t *w, const uint8_t *ws, const 
     if (rows < 1 || slots < 1 || slots > BQM_EXPERT_GEMV_MAX_SLOTS || slots % rows != 0) return BQM_EINVAL;
     if (groups < 1 || groups > BQM_MAX_GROUPS || k < 32 || n < 1 || (glu && n % 2 != 0)) return BQM_EINVAL;
     if (k % 32 != 0 || k > BQM_EXPERT_GEMV_MAX_K) return BQM_EUNSUPPORTED;
-    // whole units, as many as loads and loops look ahead, in 31 bits (half of n with the gate)
-    if (!glu && n > 0x7FFFFFFF - 4 * kEvWaves * 32) return BQM_EUNSUPPORTED;
     if (!aligned(w, 16) || !aligned(x, 16) || !aligned(ids, 4) || !aligned(y, 4)) return BQM_EUNSUPPORTED;
     const bool wide = k % 128 == 0 && aligned(ws, 4);
     static LaunchCache caches[2];
@@ -328,7 +328,7 @@ extern "C" int bqm_mxfp4_expert_gemv(const uint8_t *w, const uint8_t *ws, const 
     a.slices = (k + kEvSlice - 1) / kEvSlice;
     // As many distinct ids as slots choose by chance have work.
     const int per_unit = glu ? 16 : 32, cus = device_cus();
-    const int units = ((glu ? n / 2 : n) + per_unit - 1) / per_unit;
+    const int units = ((glu ? n / 2 : n) - 1) / per_unit + 1;
     double distinct = slots;
     if (rows > 1) {
         double missed = 1.0;

@@ -119,10 +119,9 @@ int bqm_mxfp4_grouped_gemm(const uint8_t *w, const uint8_t *ws, const uint8_t *x
  *   x   : f32 [rows][k], 16-byte aligned, dense.
  *   ids : int32 [slots]; a slot whose id is outside 0..groups-1 gets zeros.
  *   y   : f32 [slots][n or n/2] out.
- *   1 <= slots <= BQM_EXPERT_GEMV_MAX_SLOTS (else BQM_EINVAL), k <=
- *   BQM_EXPERT_GEMV_MAX_K, n < 2^31 - 1024 without the gate (else
- *   BQM_EUNSUPPORTED); the rest as bqm_mxfp4_grouped_gemm, scales as in
- *   bqm_mxfp4_gemv.
+ *   1 <= slots <= BQM_EXPERT_GEMV_MAX_SLOTS, k <= BQM_EXPERT_GEMV_MAX_K (else
+ *   BQM_EUNSUPPORTED for k, BQM_EINVAL for slots), any n; the rest as
+ *   bqm_mxfp4_grouped_gemm, scales as in bqm_mxfp4_gemv.
  */
 int bqm_mxfp4_expert_gemv(const uint8_t *w, const uint8_t *ws, const float *x, const int *ids, float *y, int glu,
                           int rows, int slots, int groups, int k, int n, void *stream);

@@ -24,9 +24,10 @@ def bqm():
     torch.cuda.empty_cache()
 
 
-@pytest.mark.parametrize("glu,n", [(False, 2 ** 31 - 1025), (True, 2 ** 31 - 2)])
+@pytest.mark.parametrize("glu,n", [(False, 2 ** 31 - 1025), (False, 2 ** 31 - 513), (False, 2 ** 31 - 32), (False, 2 ** 31 - 1), (True, 2 ** 31 - 2)])
 def test_expert_gemv_the_most_weight_rows(bqm, glu, n):
-    """34 GB of codes; a second slot of no expert, all zeros to the last output."""
+    """34 GB of codes; a second slot of no expert, all zeros to the last output.  Rounded up to units of 32 rows the
+    largest n leave 31 bits, and the last 512 outputs end a workgroup's steps past them."""
     k, outs = 32, n // 2 if glu else n
     w = torch.full((1, n, k // 2), 0x22, dtype=torch.uint8, device=DEV)
     ws = torch.full((1, n, 1), 122, dtype=torch.uint8, device=DEV)

@@ -22,13 +22,6 @@ def L():
     return bqm.lib()
 
 
-@pytest.mark.parametrize("rows,slots", [(1, 1), (4, 4), (16, 64)])
-def test_expert_gemv_rows_that_round_up_past_31_bits(L, rows, slots):
-    """Rounded up to units of 32 rows their count wraps; the last 512 also end a workgroup's loop over a row past it."""
-    for n in (MOST, MOST - 15, MOST - 30, MOST - 31, MOST - 511, MOST - 1023):
-        assert L.bqm_mxfp4_expert_gemv(A, B, C, D, E, 0, rows, slots, 3, 32, n, NUL) == 2
-
-
 def test_lora_add_rows_and_widths_past_the_grid(L):
     def f(m, k=64, n=8, adapters=1):
         return L.bqm_lora_add(A, k, 0, B, C, 2, NUL, D, E, NUL, n, F, n, A, m, k, n, 8, adapters, NUL)
